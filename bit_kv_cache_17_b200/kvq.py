@@ -22,6 +22,7 @@ TYPES = {
 }
 KVQ_OK, KVQ_E_INVAL, KVQ_E_UNSUPPORTED, KVQ_E_CAPACITY = 0, -1, -2, -3
 KVQ_E_ALIGN, KVQ_E_CUDA, KVQ_E_DEVICE, KVQ_E_SIZE = -4, -5, -6, -7
+KVQ_DT_F32, KVQ_DT_BF16, KVQ_DT_F16 = 0, 1, 2
 
 
 class kvq_params(C.Structure):
@@ -30,6 +31,13 @@ class kvq_params(C.Structure):
         ("head_dim", C.c_int32), ("max_ctx", C.c_int64), ("type_k", C.c_int32),
         ("type_v", C.c_int32), ("tail", C.c_int32), ("group", C.c_int32),
         ("sinkhorn_iters", C.c_int32), ("page_tokens", C.c_int32), ("var_norm", C.c_int32), ("tail_f16", C.c_int32),
+    ]
+
+
+class kvq_rope_params(C.Structure):
+    _fields_ = [
+        ("rot_dim", C.c_int32), ("n_axes", C.c_int32), ("sections", C.c_int32 * 4), ("turns", C.c_int32),
+        ("adjacent", C.c_int32), ("inverse", C.c_int32), ("theta", C.c_double),
     ]
 
 
@@ -61,6 +69,17 @@ _SIG = {
     "kvq_strerror": (C.c_char_p, [C.c_int]),
     "kvq_launch_count": (C.c_int, [C.POINTER(C.c_uint64)]),
     "kvq_decode_attn_noalloc": (C.c_int, [_vp, _i32, _i32, C.POINTER(_i32), _i32, _vp, C.c_float, _vp, _vp]),
+    "kvq_rope_default_params": (None, [C.POINTER(kvq_rope_params)]),
+    "kvq_rope": (C.c_int, [C.POINTER(kvq_rope_params), C.POINTER(C.c_double), _i64, _vp, _i64, _i32, _vp, _i32, _i64,
+                           _vp, _i32, _i64, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "kvq_batch_workspace_bytes": (C.c_int, [_vp, _i32, _i32, C.POINTER(_i32), C.POINTER(_i32), _i32, C.POINTER(_sz)]),
+    "kvq_batch_attn": (C.c_int, [_vp, _i32, _i32, C.POINTER(_i32), C.POINTER(_i32), _i32, _i32, _vp, C.c_float, _vp,
+                                 _vp, _vp, _sz, _vp]),
+    "kvq_attn_mass": (C.c_int, [_vp, _i32, _i32, C.POINTER(_i32), C.POINTER(_i32), _i32, _i32, _vp, C.c_float, _vp,
+                                C.c_float, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "kvq_evict_workspace_bytes": (C.c_int, [_vp, _vp, _i32, _i32, C.POINTER(_sz)]),
+    "kvq_evict": (C.c_int, [_vp, _i32, _vp, _i32, _i32, C.POINTER(_i32), C.POINTER(_i32), _vp, _i64, _i32, _i32, _i32,
+                            _vp, _vp, _i64, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -153,6 +172,61 @@ def kvq_decode_attn_noalloc(h, layer, seq_ids, n_q_heads, q_ptr, softmax_scale, 
     _check(rc, "kvq_decode_attn_noalloc")
 
 
+def kvq_rope_default_params(**overrides):
+    p = kvq_rope_params()
+    _lib.kvq_rope_default_params(C.byref(p))
+    for k, v in overrides.items():
+        if k == "sections":
+            v = (_i32 * 4)(*v)
+        setattr(p, k, v)
+    return p
+
+
+def kvq_rope(p, inv_freq, n_tokens, pos_ptr, pos_ld, n_q_heads, q_ptr, q_type, q_ld, q_out_ptr, q_out_type, q_out_ld,
+             n_k_heads, k_ptr, k_ld, k_out_ptr, k_out_ld, stream=0):
+    """inv_freq: None or a ctypes array of rot_dim / 2 doubles"""
+    rc = _lib.kvq_rope(C.byref(p), inv_freq, n_tokens, _vp(pos_ptr), pos_ld, n_q_heads, _vp(q_ptr), q_type, q_ld,
+                       _vp(q_out_ptr), q_out_type, q_out_ld, n_k_heads, _vp(k_ptr), k_ld, _vp(k_out_ptr), k_out_ld,
+                       _vp(stream))
+    _check(rc, "kvq_rope")
+
+
+def kvq_batch_workspace_bytes(h, layer, seq_ids, n_q, n_q_heads):
+    n = _sz()
+    rc = _lib.kvq_batch_workspace_bytes(h, layer, len(seq_ids), _i32arr(seq_ids), _i32arr(n_q), n_q_heads, C.byref(n))
+    _check(rc, "kvq_batch_workspace_bytes")
+    return n.value
+
+
+def kvq_batch_attn(h, layer, seq_ids, n_q, n_q_heads, causal, q_ptr, softmax_scale, out_ptr, lse_ptr, ws_ptr, ws_bytes,
+                   stream=0):
+    rc = _lib.kvq_batch_attn(h, layer, len(seq_ids), _i32arr(seq_ids), _i32arr(n_q), n_q_heads, int(causal),
+                             _vp(q_ptr), softmax_scale, _vp(out_ptr), _vp(lse_ptr), _vp(ws_ptr), ws_bytes, _vp(stream))
+    _check(rc, "kvq_batch_attn")
+
+
+def kvq_attn_mass(h, layer, seq_ids, n_q, n_q_heads, causal, q_ptr, softmax_scale, lse_ptr, decay, mass_in_ptr,
+                  mass_out_ptr, mass_ld, ws_ptr, ws_bytes, stream=0):
+    rc = _lib.kvq_attn_mass(h, layer, len(seq_ids), _i32arr(seq_ids), _i32arr(n_q), n_q_heads, int(causal), _vp(q_ptr),
+                            softmax_scale, _vp(lse_ptr), decay, _vp(mass_in_ptr), _vp(mass_out_ptr), mass_ld,
+                            _vp(ws_ptr), ws_bytes, _vp(stream))
+    _check(rc, "kvq_attn_mass")
+
+
+def kvq_evict_workspace_bytes(src, dst, n_seqs, budget):
+    n = _sz()
+    _check(_lib.kvq_evict_workspace_bytes(src, dst, n_seqs, budget, C.byref(n)), "kvq_evict_workspace_bytes")
+    return n.value
+
+
+def kvq_evict(src, src_layer, dst, dst_layer, src_ids, dst_ids, mass_ptr, mass_ld, budget, sink, recent, kept_ptr,
+              mass_out_ptr, mass_out_ld, ws_ptr, ws_bytes, stream=0):
+    rc = _lib.kvq_evict(src, src_layer, dst, dst_layer, len(src_ids), _i32arr(src_ids), _i32arr(dst_ids),
+                        _vp(mass_ptr), mass_ld, budget, sink, recent, _vp(kept_ptr), _vp(mass_out_ptr), mass_out_ld,
+                        _vp(ws_ptr), ws_bytes, _vp(stream))
+    _check(rc, "kvq_evict")
+
+
 def kvq_dequant(h, layer, seq, which, t0, t1, basis, out_ptr, stream=0):
     _check(_lib.kvq_dequant(h, layer, seq, which, t0, t1, basis, _vp(out_ptr), _vp(stream)), "kvq_dequant")
 
@@ -185,6 +259,111 @@ def kvq_launch_count():
 
 def kvq_describe(h):
     return _lib.kvq_describe(h).decode()
+
+
+def _refuse(cond, where, why, code=KVQ_E_INVAL):
+    if cond:
+        raise KVQError(code, f"{where}: {why}")
+
+
+class _Call:
+    """Where a call's tensors are made and its kernels run: `stream` (a torch stream, or the
+    device's current one).  Outputs and workspace come from the caching allocator under that
+    stream, so calls on several streams, and captured graphs, each have their own."""
+
+    __slots__ = ("torch", "device", "stream", "inner", "outer")
+
+    def __init__(self, torch, device, stream):
+        self.torch, self.device = torch, device
+        self.outer = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.inner = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.outer is not None:
+            self.outer.__enter__()
+        if self.inner is not None:
+            self.inner.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+        if self.outer is not None:
+            self.outer.__exit__(*exc)
+
+
+class Rope:
+    """Rotary positions with several axes (kvq_rope): what a model fixes once.
+
+    sections: channel pairs of each axis, in the order of the rows of `pos`; `turns`: the axes take
+    turns pair by pair instead of following one another; `adjacent`: pairs (2i, 2i+1) instead of
+    (i, i + rot_dim/2); inv_freq: rot_dim/2 frequencies instead of theta's.
+    """
+
+    def __init__(self, sections=(64,), theta=10000.0, rot_dim=None, turns=False, adjacent=False, inv_freq=None):
+        import torch
+
+        self.torch = torch
+        sections = [int(x) for x in sections]
+        _refuse(not 1 <= len(sections) <= 4, "Rope", "1 to 4 sections")
+        rot_dim = 2 * sum(sections) if rot_dim is None else int(rot_dim)
+        self.n_axes = len(sections)
+        self._p = [kvq_rope_default_params(rot_dim=rot_dim, n_axes=self.n_axes,
+                                           sections=sections + [0] * (4 - len(sections)), turns=int(turns),
+                                           adjacent=int(adjacent), inverse=i, theta=float(theta)) for i in (0, 1)]
+        self._freq = None
+        if inv_freq is not None:
+            f = [float(x) for x in inv_freq]
+            _refuse(len(f) != rot_dim // 2, "Rope", "inv_freq holds rot_dim / 2 values")
+            self._freq = (C.c_double * len(f))(*f)
+        self._types = {torch.float32: KVQ_DT_F32, torch.bfloat16: KVQ_DT_BF16, torch.float16: KVQ_DT_F16}
+        # the host checks of the parameters, once: a call over no tokens
+        kvq_rope(self._p[0], self._freq, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+
+    def _rows(self, x, n, name):
+        _refuse(x.dim() != 3 or x.shape[0] != n or x.shape[2] != 128 or x.stride(2) != 1 or
+                (x.shape[1] > 1 and x.stride(1) != 128), "Rope.apply",
+                f"{name} is [tokens, heads, 128] with contiguous heads")
+        # the row stride of a single token says nothing
+        return x.stride(0) if n > 1 else max(x.stride(0), x.shape[1] * 128)
+
+    def apply(self, pos, q=None, k=None, q_dtype=None, inverse=False, q_out=None, k_out=None, stream=None):
+        """pos: int32 [n_axes, tokens] (or [tokens] for one axis); q: [tokens, heads, 128] fp32, BF16
+        or F16, a slice of a packed row allowed; k: BF16 likewise.  Returns (q_out, k_out), new
+        contiguous tensors (q of q_dtype, its own type by default) unless given; an output may be its
+        input."""
+        torch = self.torch
+        if pos.dim() == 1:
+            pos = pos[None]
+        _refuse(pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[0] != self.n_axes, "Rope.apply",
+                "pos is int32 [n_axes, tokens]")
+        n = pos.shape[1]
+        _refuse(n > 1 and pos.stride(1) != 1, "Rope.apply", "the tokens of pos are contiguous")
+        pos_ld = pos.stride(0) if self.n_axes > 1 else n
+        for x in (q, k, q_out, k_out):
+            _refuse(x is not None and x.device != pos.device, "Rope.apply", "tensors on different devices")
+        _refuse(pos.device.type != "cuda", "Rope.apply", "tensors are on a CUDA device")
+        with _Call(torch, pos.device, stream) as st:
+            a, b = (0, 0, 0, 0, 0, 0, 0), (0, 0, 0, 0, 0)
+            if q is not None:
+                if q_out is None:
+                    q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
+                _refuse(q.dtype not in self._types or q_out.dtype not in self._types or
+                        (q_dtype is not None and q_out.dtype != q_dtype), "Rope.apply", "type of q",
+                        KVQ_E_UNSUPPORTED)
+                _refuse(q_out.shape != q.shape, "Rope.apply", "q_out has q's shape")
+                a = (q.shape[1], q.data_ptr(), self._types[q.dtype], self._rows(q, n, "q"), q_out.data_ptr(),
+                     self._types[q_out.dtype], self._rows(q_out, n, "q_out"))
+            if k is not None:
+                if k_out is None:
+                    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+                _refuse(k.dtype != torch.bfloat16 or k_out.dtype != torch.bfloat16, "Rope.apply", "k is BF16",
+                        KVQ_E_UNSUPPORTED)
+                _refuse(k_out.shape != k.shape, "Rope.apply", "k_out has k's shape")
+                b = (k.shape[1], k.data_ptr(), self._rows(k, n, "k"), k_out.data_ptr(), self._rows(k_out, n, "k_out"))
+            kvq_rope(self._p[int(bool(inverse))], self._freq, n, pos.data_ptr(), max(pos_ld, n), *a, *b, st)
+        return q_out, k_out
 
 
 class KVCache:
@@ -267,6 +446,125 @@ class KVCache:
         kvq_prefill_attn(self.handle, layer, seq, n_q, n_q_heads, q.data_ptr(), softmax_scale, out.data_ptr(),
                          ws.data_ptr(), ws.numel(), self._stream(stream))
         return out
+
+    def rows16(self, layer):
+        """The 16-bit rows of a layer, a view of the storage [n_seqs, n_kv_heads, 2 (K, V), ring rows, 128]
+        in the tail's type: token p of a sequence in row p mod the ring rows."""
+        torch, p = self.torch, self.params
+        kvarn = any(8 <= t <= 13 or (p.var_norm and t != 0) for t in (p.type_k, p.type_v))
+        rows = p.max_ctx if p.type_k == 0 else p.tail + (256 if kvarn else 0)
+        _refuse(rows == 0, "rows16", "a cache without a 16-bit tail")
+        off, _ = kvq_locate(self.handle, 1, layer, 0, 0, 0, 0, 0)
+        n = p.n_seqs * p.n_kv_heads * 2 * rows * 128
+        x = self.storage[off:off + 2 * n].view(torch.float16 if p.tail_f16 else torch.bfloat16)
+        return x.view(p.n_seqs, p.n_kv_heads, 2, rows, 128)
+
+    def _same_device(self, x, where, name):
+        _refuse(x.device != self.storage.device, where, f"{name} is on another device than the cache")
+
+    def _queries(self, where, q, n_q):
+        torch = self.torch
+        _refuse(q.dtype != (torch.float16 if self.params.tail_f16 else torch.bfloat16), where,
+                "q is in the cache's 16-bit type (BF16, or F16 with tail_f16)", KVQ_E_UNSUPPORTED)
+        _refuse(q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous() or q.shape[0] != sum(n_q), where,
+                "q is contiguous [sum(n_q), n_q_heads, 128]")
+        self._same_device(q, where, "q")
+
+    def batch_attn(self, layer, seq_ids, n_q, q, causal=False, out=None, lse=None, return_lse=False, softmax_scale=0.0,
+                   stream=None):
+        """kvq_batch_attn: q [sum(n_q), n_q_heads, 128] in the cache's 16-bit type, n_q[i] query tokens
+        over sequence seq_ids[i]; every token seen (cross attention), or causal over the newest n_q[i].
+        Returns out, or (out, lse [sum(n_q), n_q_heads] fp32) with return_lse or a given lse."""
+        torch = self.torch
+        seq_ids, n_q = list(seq_ids), list(n_q)
+        _refuse(len(seq_ids) != len(n_q), "batch_attn", "one n_q for each sequence")
+        self._queries("batch_attn", q, n_q)
+        hq = q.shape[1]
+        with _Call(torch, self.storage.device, stream) as st:
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None and return_lse:
+                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+            _refuse(out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous(), "batch_attn",
+                    "out has q's shape and type")
+            self._same_device(out, "batch_attn", "out")
+            if lse is not None:
+                self._lse("batch_attn", lse, q)
+            nb = kvq_batch_workspace_bytes(self.handle, layer, seq_ids, n_q, hq)
+            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
+            kvq_batch_attn(self.handle, layer, seq_ids, n_q, hq, causal, q.data_ptr(), softmax_scale, out.data_ptr(),
+                           0 if lse is None else lse.data_ptr(), ws.data_ptr(), nb, st)
+        return out if lse is None else (out, lse)
+
+    def _lse(self, where, lse, q):
+        _refuse(lse.dtype != self.torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous(),
+                where, "lse is contiguous fp32 [sum(n_q), n_q_heads]")
+        self._same_device(lse, where, "lse")
+
+    def _mass_rows(self, where, x, n, name):
+        p = self.params
+        _refuse(x.dtype != self.torch.float32 or x.dim() != 3 or x.shape[0] != n or x.shape[1] != p.n_kv_heads or
+                not x.is_contiguous(), where, f"{name} is contiguous fp32 [sequences, n_kv_heads, tokens]")
+        self._same_device(x, where, name)
+
+    def attn_mass(self, layer, seq_ids, n_q, q, lse, causal=False, decay=1.0, mass_in=None, mass_out=None,
+                  softmax_scale=0.0, stream=None):
+        """kvq_attn_mass: the weight each cached token gets from these query rows (lse as batch_attn
+        returned it), summed over the query heads of its KV head, on top of decay * mass_in.
+        mass_in, mass_out: fp32 [len(seq_ids), n_kv_heads, tokens >= the longest sequence]; mass_out
+        defaults to a new tensor (zeros behind each sequence); both may be one tensor."""
+        torch = self.torch
+        seq_ids, n_q = list(seq_ids), list(n_q)
+        _refuse(len(seq_ids) != len(n_q), "attn_mass", "one n_q for each sequence")
+        self._queries("attn_mass", q, n_q)
+        self._lse("attn_mass", lse, q)
+        hq = q.shape[1]
+        if mass_in is None:
+            decay = 0.0
+        else:
+            self._mass_rows("attn_mass", mass_in, len(seq_ids), "mass_in")
+        with _Call(torch, self.storage.device, stream) as st:
+            if mass_out is None:
+                most = max([self.seq_len(layer, s) for s in seq_ids] + [1])
+                shape = (len(seq_ids), self.params.n_kv_heads, most) if mass_in is None else mass_in.shape
+                mass_out = torch.zeros(shape, dtype=torch.float32, device=self.storage.device)
+            self._mass_rows("attn_mass", mass_out, len(seq_ids), "mass_out")
+            _refuse(mass_in is not None and mass_in.shape != mass_out.shape, "attn_mass", "mass_in has mass_out's shape")
+            nb = kvq_batch_workspace_bytes(self.handle, layer, seq_ids, n_q, hq)
+            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
+            kvq_attn_mass(self.handle, layer, seq_ids, n_q, hq, causal, q.data_ptr(), softmax_scale, lse.data_ptr(),
+                          decay, 0 if mass_in is None else mass_in.data_ptr(), mass_out.data_ptr(), mass_out.shape[2],
+                          ws.data_ptr(), nb, st)
+        return mass_out
+
+    def evict(self, dst, layer, dst_layer, seq_ids, dst_ids, mass, budget, sink=0, recent=0, kept=None, mass_out=None,
+              stream=None):
+        """kvq_evict: sequences dst_ids of the cache `dst` (any type) become the `budget` tokens that
+        matter of this BF16 cache's seq_ids: per KV head the first `sink`, the last `recent` and those
+        with the largest mass [len(seq_ids), n_kv_heads, tokens] of the others.  Returns (kept int32
+        [len(seq_ids), n_kv_heads, budget], -1 behind the last; mass_out fp32 of the same shape, zeros
+        behind the last)."""
+        torch = self.torch
+        seq_ids, dst_ids = list(seq_ids), list(dst_ids)
+        n = len(seq_ids)
+        _refuse(len(dst_ids) != n, "evict", "one destination for each sequence")
+        self._mass_rows("evict", mass, n, "mass")
+        hkv = self.params.n_kv_heads
+        with _Call(torch, self.storage.device, stream) as st:
+            if kept is None:
+                kept = torch.empty((n, hkv, max(budget, 0)), dtype=torch.int32, device=self.storage.device)
+            if mass_out is None:
+                mass_out = torch.empty((n, hkv, max(budget, 0)), dtype=torch.float32, device=self.storage.device)
+            _refuse(kept.dtype != torch.int32 or tuple(kept.shape) != (n, hkv, budget) or not kept.is_contiguous(),
+                    "evict", "kept is contiguous int32 [sequences, n_kv_heads, budget]")
+            self._same_device(kept, "evict", "kept")
+            self._mass_rows("evict", mass_out, n, "mass_out")
+            nb = kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget)
+            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=self.storage.device)
+            kvq_evict(self.handle, layer, dst.handle, dst_layer, seq_ids, dst_ids, mass.data_ptr(), mass.shape[2],
+                      budget, sink, recent, kept.data_ptr(), mass_out.data_ptr(), mass_out.shape[2], ws.data_ptr(), nb,
+                      st)
+        return kept, mass_out
 
     def dequant(self, layer, seq, which, t0, t1, basis=0, out=None, stream=None):
         if out is None:

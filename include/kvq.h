@@ -270,6 +270,102 @@ int kvq_decode_attn_noalloc(kvq_cache *c, int32_t layer, int32_t n_seqs, const i
                             int32_t n_q_heads, const float *q, float softmax_scale, float *out,
                             kvq_stream_t stream);
 
+/* Element types of the 16- and 32-bit rows that kvq_rope reads and writes. */
+typedef enum kvq_dtype { KVQ_DT_F32 = 0, KVQ_DT_BF16 = 1, KVQ_DT_F16 = 2 } kvq_dtype;
+
+/* Rotary positions with several axes (images: height, width; video: time, height, width).
+ * Channel pair i < rot_dim / 2 of a head belongs to one axis a(i) and turns by
+ * angle(t, i) = pos[a(i)][t] * f_i,  f_i = theta^(-2 i / rot_dim):
+ * (x, y) -> (x cos - y sin, y cos + x sin).  Channels rot_dim .. 127 pass through. */
+typedef struct kvq_rope_params {
+  int32_t rot_dim;     /* channels that turn: even, 2..128 */
+  int32_t n_axes;      /* 1..4 */
+  int32_t sections[4]; /* pairs of each axis, >= 0, rot_dim / 2 in all */
+  int32_t turns;       /* 0: the sections follow one another; 1: the axes take turns, pair by pair,
+                        * while they have pairs left */
+  int32_t adjacent;    /* 0: pair i = channels (i, i + rot_dim / 2); 1: channels (2 i, 2 i + 1) */
+  int32_t inverse;     /* 1: turn back by the same angles (undoes a rotation; also its gradient) */
+  double theta;        /* > 0 */
+} kvq_rope_params;
+
+/* Defaults: 128 channels, one axis of 64 pairs, theta 10000. */
+void kvq_rope_default_params(kvq_rope_params *p);
+
+/* Rotates the query and key rows of n_tokens tokens in one launch: the step before kvq_append and
+ * the attention calls, which take rotated rows.
+ * inv_freq: host, rot_dim / 2 frequencies f_i in place of theta's (any scaling of the base), or NULL.
+ * pos: device int32, pos[a * pos_ld + t] the position of token t on axis a (any value; the angle is
+ * reduced in 64 bits).  q: device rows [n_tokens][n_q_heads][128] of q_type, token t at element
+ * t * q_ld (a slice of a packed q|k|v row is a q_ld larger than n_q_heads * 128); q_out likewise, of
+ * q_out_type.  k, k_out: BF16 rows, as kvq_append takes them.  n_q_heads or n_k_heads may be 0 (its
+ * pointers are then not looked at).  An output may be its own input (same type and ld); otherwise
+ * the spans from the first to the last row of the two must not overlap (KVQ_E_INVAL).  Pointers and
+ * row strides are multiples of 16 bytes (KVQ_E_ALIGN; pos: 4).  Arithmetic is fp32 with one rounding
+ * to the output type; channels that pass through are converted only.  Runs on the current device. */
+int kvq_rope(const kvq_rope_params *p, const double *inv_freq, int64_t n_tokens, const int32_t *pos,
+             int64_t pos_ld, int32_t n_q_heads, const void *q, int32_t q_type, int64_t q_ld, void *q_out,
+             int32_t q_out_type, int64_t q_out_ld, int32_t n_k_heads, const void *k, int64_t k_ld,
+             void *k_out, int64_t k_out_ld, kvq_stream_t stream);
+
+/* Workspace bytes kvq_batch_attn and kvq_attn_mass need for these sequences and query counts
+ * (host arithmetic on the current lengths; growing sequences may need more). */
+int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids,
+                              const int32_t *n_q, int32_t n_q_heads, size_t *bytes);
+
+/* Attention of many query rows over cached sequences: cross attention of decoder rows to encoder
+ * states kept in a cache (causal = 0: every row sees every token of its sequence), or the prefill
+ * of a ragged batch of prompts (causal = 1: row i of entry e sees the first n - n_q[e] + 1 + i
+ * tokens, n_q[e] <= n).  Entry e is n_q[e] >= 0 query tokens over sequence seq_ids[e]; a sequence may
+ * be listed several times (beams over one encoder state).
+ * q: device [sum(n_q), n_q_heads, 128] in the cache's 16-bit format (BF16, or F16 with tail_f16),
+ * the rows of entry 0 first; out: same shape and type; lse: device fp32 [sum(n_q), n_q_heads] or
+ * NULL: log of the sum of exp(scale q.k) of each row.  softmax_scale <= 0 selects 1/sqrt(128).
+ * A row that sees no token gives zeros and lse = -inf.  workspace: device, >=
+ * kvq_batch_workspace_bytes.  Scores, the softmax and both sums are fp32; the weights are rounded to
+ * the 16-bit type of the matrix product.  A BF16 cache (either tail format) is read as it is; the
+ * values of a quantized cache are first rebuilt in the original basis in F16, in the workspace
+ * (values and queries must then lie within the F16 range).  kvq_decode_attn remains the call for
+ * one fp32 query row per quantized sequence. */
+int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids, const int32_t *n_q,
+                   int32_t n_q_heads, int32_t causal, const void *q, float softmax_scale, void *out, float *lse,
+                   void *workspace, size_t ws_bytes, kvq_stream_t stream);
+
+/* The attention weight each cached token receives from the same query rows, given their lse:
+ * mass_out[e][h][t] = decay * mass_in[e][h][t] + sum over the rows of entry e and the query heads
+ * of KV head h that see token t of exp(scale q.k - lse), for t < n; places behind the sequence's
+ * last token are left as they were.  mass_in, mass_out: device fp32, [n_seqs][n_kv_heads][mass_ld],
+ * mass_ld >= the longest listed sequence; mass_out may be mass_in; decay in [0, 1], and with decay 0
+ * mass_in is not read (NULL allowed).  lse: as kvq_batch_attn (or any call over the same rows)
+ * wrote it; rows with lse = -inf weigh nothing.  The other arguments are kvq_batch_attn's. */
+int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids, const int32_t *n_q,
+                  int32_t n_q_heads, int32_t causal, const void *q, float softmax_scale, const float *lse,
+                  float decay, const float *mass_in, float *mass_out, int64_t mass_ld, void *workspace,
+                  size_t ws_bytes, kvq_stream_t stream);
+
+/* Workspace bytes kvq_evict needs: the kept indices, and for a quantized destination the kept rows. */
+int kvq_evict_workspace_bytes(const kvq_cache *src, const kvq_cache *dst, int32_t n_seqs, int32_t budget,
+                              size_t *bytes);
+
+/* Cuts sequences down to the tokens that matter, by accumulated attention weight: sequence
+ * dst_ids[e] of dst becomes what appending the kept tokens of sequence src_ids[e], in their order, to
+ * an empty sequence would make it (so dst may be of any type, quantized ones included).
+ * Of a sequence of n > budget tokens every KV head keeps, for itself, the first `sink`, the last
+ * `recent` and, of the others, the budget - sink - recent with the largest mass[e][h][t] (equal
+ * weights: the lower index first; NaN counts as larger than any number).  n <= budget: all of them.
+ * The new length is min(n, budget), known on the host when the call returns.
+ * src: a BF16 cache (KVQ_E_UNSUPPORTED for quantized types, whose values would be quantized twice).
+ * mass: device fp32 [n_seqs][n_kv_heads][mass_ld], mass_ld >= every n.  kept: device int32
+ * [n_seqs][n_kv_heads][budget] or NULL: the kept tokens' old indices in ascending order, -1 behind
+ * them.  mass_out: device fp32 [n_seqs][n_kv_heads][mass_out_ld >= budget] or NULL: the kept
+ * tokens' weights, zeros behind them.  Neither may overlap mass.  dst_ids are distinct; with dst ==
+ * src and the same layer none of them may be among src_ids (KVQ_E_INVAL).  sink + recent <= budget.
+ * Keys keep the rotation they were appended with; positions of later tokens are the caller's
+ * (kvq_rope takes them explicitly). */
+int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int32_t dst_layer, int32_t n_seqs,
+              const int32_t *src_ids, const int32_t *dst_ids, const float *mass, int64_t mass_ld, int32_t budget,
+              int32_t sink, int32_t recent, int32_t *kept, float *mass_out, int64_t mass_out_ld, void *workspace,
+              size_t ws_bytes, kvq_stream_t stream);
+
 /* Diagnostic: number of kernels this library has launched (or recorded into a CUDA graph
  * under stream capture) in this process, across all caches. */
 int kvq_launch_count(uint64_t *count);
