@@ -7,9 +7,11 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_codes.cuh"
 #include "kvq_internal.h"
+#include "kvq_tc.cuh"
 
 using namespace kvq;
 
@@ -18,19 +20,29 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAXE = 64;  // entries per launch
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
 
 // One entry: nq query tokens from row token q0 on, over the first n rows of stream `slot`.
 struct BEntry {
   int32_t slot, seq, nq;
-  int32_t out;  // position in the call's list (mass rows)
+  int32_t out;      // position in the call's list (mass rows)
   int64_t n, q0;
+  int32_t nblk;     // blocks of query tokens
+  int32_t nsplit;   // splits of the key tiles
+  int32_t cps;      // key tiles per split
+  int32_t halves;   // one query tile: the two softmax groups take the even and the odd key tiles
+  int32_t cta0;     // first CTA
+  int64_t part0;    // first partial record (nsplit > 1)
 };
 
-// 16-bit K and V rows: row t of (slot, head, which) at ((slot * hkv + head) * 2 + which) * cap + t
+// 16-bit rows: row t of (slot, head, side) at ((slot * hkv + head) * sides + side) * cap + t; K is
+// side 0, V the last; a rebuilt cache has the keys' remainders in between.
 struct Source {
   const uint16_t *base;
   int64_t cap;
-  int32_t f16;  // element type: F16, else BF16
+  int32_t slots;
+  int32_t f16;    // element type: F16, else BF16
+  int32_t sides;  // 2 or 3
 };
 
 struct BArgs {
@@ -44,11 +56,13 @@ struct BArgs {
   float *mass_out;
   int64_t mass_ld;
   float decay;
+  float *part;
+  int32_t *status;
   BEntry e[MAXE];
 };
 
-__device__ __forceinline__ const uint16_t *kv_row(const BArgs &A, int slot, int head, int which, int64_t t) {
-  return A.src.base + ((((int64_t)slot * A.hkv + head) * 2 + which) * A.src.cap + t) * D;
+__device__ __forceinline__ const uint16_t *kv_row(const BArgs &A, int slot, int head, int side, int64_t t) {
+  return A.src.base + ((((int64_t)slot * A.hkv + head) * A.src.sides + side) * A.src.cap + t) * D;
 }
 
 __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4]) {
@@ -63,36 +77,466 @@ __device__ __forceinline__ float dot4(const float (&a)[4], const float (&b)[4]) 
   return s;
 }
 
-// One warp per (query token, query head).
-__global__ void __launch_bounds__(256) k_attn_rows(const __grid_constant__ BArgs A, int64_t items) {
+// ---- attention ------------------------------------------------------------------------------------
+//
+// One CTA per (entry, KV head, block of query tokens, split of the key tiles).  A tile of 128 rows
+// holds the G query heads of floor(128 / G) tokens (row = token * G + head), so one K/V tile serves
+// all of them; a block is two such tiles, or one when the entry has no more rows.
+//  - a load warp fetches 128-token K and V tiles (32 KB each) with TMA into a ring of stages;
+//  - one thread issues S = Q.K^T (M = N = 128, SS) and O += P.V (P from tensor memory, V as the
+//    MN-major operand straight from the rows), S, P and O in tensor memory: 512 columns;
+//  - two softmax groups of four warps, thread = row = tensor-memory lane: group t owns query tile t
+//    (two tiles), or the key tiles j = t mod 2 (one tile: `halves`, joined in shared memory at the
+//    end).  While one group works on its scores the tensor core runs the other's products.
+//  - the running maximum moves only when a score passes it by 2^8 (the weights stay below 2^8, O is
+//    rescaled in tensor memory then), so most tiles need no correction.
+// Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
+constexpr int BT = 128;            // rows of a query tile, tokens of a key tile
+constexpr int NSOFT = 8;           // softmax warps
+constexpr int W_MMA = 8, W_LOAD = 9;
+constexpr int NT = 320;
+constexpr int TILE = BT * D * 2;   // bytes of a tile
+constexpr int HALF = TILE / 2;     // 64 channels of it
+constexpr int MAXST = 6;           // stages
+constexpr float TAU = 8.f;         // lazy maximum, log2 units
+constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
+constexpr int MAXSPL = 64;
+
+struct Ctl {
+  uint64_t full[MAXST], empty[MAXST], tmp;
+  uint64_t s_full[2], p_full[2], o_full;
+  uint32_t tmem;
+  int32_t abort;
+};
+constexpr int OFF_CTL = 7 * TILE;  // two or one query tiles and five or six stages
+constexpr int ATTN_SMEM = OFF_CTL + (int)sizeof(Ctl) + 1024;
+static_assert(ATTN_SMEM <= 232448, "shared memory per CTA");
+
+// The visible tokens of query token i of an entry.
+__device__ __forceinline__ int64_t limit_of(const BArgs &A, const BEntry &e, int i) {
+  return A.causal ? e.n - e.nq + 1 + i : e.n;
+}
+
+// Copies query rows [row of the tile] of one tile into the swizzled layout (two 64-channel halves);
+// rows past the last are zero.  F16 products over BF16 rows convert (exact in the F16 range).
+template <bool F16>
+__device__ __forceinline__ void load_q_row(const BArgs &A, const uint16_t *src, uint8_t *tile, int r) {
+  uint8_t *dst = tile + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (src) v = __ldg(reinterpret_cast<const uint4 *>(src) + 8 * h + c);
+      if (F16 && !A.io_f16) v = bf16x8_to_ring(v, 1);
+      *reinterpret_cast<uint4 *>(dst + h * HALF + ((c ^ (r & 7)) << 4)) = v;
+    }
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map, const __grid_constant__ BArgs A) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *S = smem_raw + (base - raw);
+  Ctl &C = *reinterpret_cast<Ctl *>(S + OFF_CTL);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int ei = 0;
+  while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
+  const BEntry &e = A.e[ei];
+  const int G = A.G, hq = A.hkv * G, TB = BT / G;
+  const int local = blockIdx.x - e.cta0;
+  const int sp = local % e.nsplit, head = local / e.nsplit % A.hkv;
+  const int blk = e.nblk - 1 - local / e.nsplit / A.hkv;  // the last (causal: longest) first
+  const bool halves = e.halves;
+  const int ntile = halves ? 1 : 2;  // query tiles
+  const int tok0 = blk * ntile * TB, tok1 = min(e.nq, tok0 + ntile * TB);
+  const int64_t lim_max = limit_of(A, e, tok1 - 1);
+  const int kt = (int)((lim_max + BT - 1) / BT);
+  const int j0 = sp * e.cps, nt = max(0, min(e.cps, kt - j0));
+  const int nst = halves ? 6 : 5;
+  const uint32_t stage0 = base + ntile * TILE;
+  const bool lo = A.src.sides == 3;
+  const uint32_t cb = tc::smem_u32(&C);
+  const uint32_t b_full = cb + (uint32_t)offsetof(Ctl, full), b_empty = cb + (uint32_t)offsetof(Ctl, empty);
+  const uint32_t b_s = cb + (uint32_t)offsetof(Ctl, s_full), b_p = cb + (uint32_t)offsetof(Ctl, p_full);
+  const uint32_t b_o = cb + (uint32_t)offsetof(Ctl, o_full), b_tmp = cb + (uint32_t)offsetof(Ctl, tmp);
+  volatile int32_t *abort = &C.abort;
+
+  if (warp == W_LOAD && lane == 0) {
+    for (int i = 0; i < MAXST; ++i) {
+      tc::mbar_init(b_full + 8 * i, 1);
+      tc::mbar_init(b_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(b_s + 8 * i, 1);
+      tc::mbar_init(b_p + 8 * i, 4);
+    }
+    tc::mbar_init(b_o, 1);
+    tc::mbar_init(b_tmp, 1);
+    C.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == W_MMA) tc::tmem_alloc(cb + (uint32_t)offsetof(Ctl, tmem), 512);
+  if (warp < NSOFT) {
+    const int t = warp >> 2, r = tid & 127;
+    if (t < ntile) {
+      const int i = tok0 + t * TB + r / G;
+      const bool on = r < TB * G && i < tok1;
+      load_q_row<F16>(A, on ? A.q + ((e.q0 + i) * hq + head * G + r % G) * D : nullptr, S + t * TILE, r);
+    }
+    tc::fence_async_smem();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = C.tmem;
+  const int z0 = (e.slot * A.hkv + head) * A.src.sides, zv = z0 + A.src.sides - 1;
+
+  if (warp == W_LOAD) {
+    // ---- K and V tiles in the order they are used: two tiles K0 V0 K1 V1 ..; halves K0 K1 V0 K2 V1 ..
+    int n_issued = 0;
+    auto next_stage = [&]() -> uint32_t {
+      const int st = n_issued % nst;
+      if (n_issued >= nst) tc::mbar_wait(b_empty + 8 * st, (n_issued / nst - 1) & 1, abort, A.status);
+      return (uint32_t)st;
+    };
+    auto load = [&](int j, int z, bool value) {
+      const uint32_t st = next_stage(), dst = stage0 + st * TILE;
+      const int64_t t0 = (int64_t)(j0 + j) * BT;
+      const int valid = (int)min((int64_t)BT, e.n - t0);
+      // rows past the sequence's end may hold anything: their keys are masked, their values would
+      // turn a weight of 0 into NaN, so they are zeroed before the tile is handed over
+      const bool patch = value && valid < BT;
+      const uint32_t bar = patch ? b_tmp : b_full + 8 * st;
+      if (lane == 0) {
+        tc::mbar_expect(bar, TILE);
+        tc::tma_load3(dst, &map, 0, (int)t0, z, bar);
+        tc::tma_load3(dst + HALF, &map, 64, (int)t0, z, bar);
+      }
+      if (patch) {  // (the last tile of the sequence: once per CTA)
+        tc::mbar_wait(b_tmp, 0, abort, A.status, false);
+        uint8_t *p = S + (dst - base);
+        for (int u = lane; u < (BT - valid) * 16; u += 32)
+          *reinterpret_cast<uint4 *>(p + (u & 1) * HALF + (valid + (u >> 4)) * 128 + ((u >> 1) & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_async_smem();
+        tc::mbar_arrive_warp(b_full + 8 * st);
+      }
+      __syncwarp();
+      ++n_issued;
+    };
+    auto keys = [&](int j) {
+      load(j, z0, false);
+      if (lo) load(j, z0 + 1, false);
+    };
+    if (nt > 0) keys(0);
+#pragma unroll 1
+    for (int j = 0; j < nt; ++j) {
+      if (halves && j + 1 < nt) keys(j + 1);
+      load(j, zv, true);
+      if (!halves && j + 1 < nt) keys(j + 1);
+    }
+    // no copy is in flight when the CTA ends (its pipeline may have been given up)
+    for (int i = max(0, n_issued - nst); i < n_issued; ++i)
+      tc::mbar_wait(b_full + 8 * (i % nst), (i / nst) & 1, abort, A.status, false);
+  } else if (warp == W_MMA) {
+    // ---- products
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0), idO = tc::idesc(F16, BT, D, 1);
+      int used = 0;  // stages consumed, in load order
+      auto take = [&]() -> uint32_t {
+        const int st = used % nst;
+        tc::mbar_wait(b_full + 8 * st, (used / nst) & 1, abort, A.status);
+        ++used;
+        return (uint32_t)st;
+      };
+      auto qk = [&](int t, uint32_t qtile, uint32_t st, bool first) {
+        const uint64_t q = tc::desc_sw128(qtile, 0), k = tc::desc_sw128(stage0 + st * TILE, 0);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t o = (uint64_t)((s & 3) * 2 + (s >> 2) * (HALF >> 4));  // 32 bytes along the channels
+          tc::mma_ss(tm + BT * t, q + o, k + o, idS, first && s == 0 ? 0u : 1u);
+        }
+      };
+      auto pv = [&](int t, uint32_t st, bool first) {
+        const uint64_t v = tc::desc_sw128(stage0 + st * TILE, HALF);
+#pragma unroll
+        for (int s = 0; s < BT / 16; ++s)  // 16 tokens: 8 columns of P, two groups of 8 rows of V
+          tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 8 * s, v + (uint64_t)(s * (2048 >> 4)), idO,
+                     first && s == 0 ? 0u : 1u);
+      };
+      auto wait_p = [&](int t, int j) {
+        tc::mbar_wait(b_p + 8 * t, j & 1, abort, A.status);
+        tc::fence_after();
+      };
+      if (!halves) {
+        {
+          const uint32_t k = take(), l = lo ? take() : 0;
+          tc::fence_after();
+          for (int t = 0; t < 2; ++t) {
+            qk(t, base + t * TILE, k, true);
+            if (lo) qk(t, base + t * TILE, l, false);
+            tc::commit(b_s + 8 * t);
+          }
+          tc::commit(b_empty + 8 * k);
+          if (lo) tc::commit(b_empty + 8 * l);
+        }
+#pragma unroll 1
+        for (int j = 0; j < nt; ++j) {
+          const bool more = j + 1 < nt;
+          const uint32_t v = take();
+          wait_p(0, j);
+          pv(0, v, j == 0);
+          uint32_t k = 0, l = 0;
+          if (more) {
+            k = take();
+            if (lo) l = take();
+            tc::fence_after();
+            qk(0, base, k, true);
+            if (lo) qk(0, base, l, false);
+            tc::commit(b_s);
+          }
+          wait_p(1, j);
+          pv(1, v, j == 0);
+          tc::commit(b_empty + 8 * v);
+          if (more) {
+            qk(1, base + TILE, k, true);
+            if (lo) qk(1, base + TILE, l, false);
+            tc::commit(b_s + 8);
+            tc::commit(b_empty + 8 * k);
+            if (lo) tc::commit(b_empty + 8 * l);
+          }
+        }
+      } else {
+        auto keys = [&](int j) {
+          const uint32_t k = take(), l = lo ? take() : 0;
+          tc::fence_after();
+          qk(j & 1, base, k, true);
+          if (lo) qk(j & 1, base, l, false);
+          tc::commit(b_s + 8 * (j & 1));
+          tc::commit(b_empty + 8 * k);
+          if (lo) tc::commit(b_empty + 8 * l);
+        };
+        // S and P of a group share columns: the scores of tile j + 2 follow the product of tile j
+        keys(0);
+        if (nt > 1) keys(1);
+#pragma unroll 1
+        for (int j = 0; j < nt; ++j) {
+          const uint32_t v = take();
+          wait_p(j & 1, j >> 1);
+          pv(j & 1, v, j < 2);
+          tc::commit(b_empty + 8 * v);
+          if (j + 2 < nt) keys(j + 2);
+        }
+      }
+      tc::commit(b_o);
+      tc::mbar_wait(b_o, 0, abort, A.status, false);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = row of query tile t (halves: of the one tile)
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tm + lanes + BT * t, tO = tm + lanes + 2 * BT + D * t;
+    const int i = tok0 + (halves ? 0 : t * TB) + r / G;
+    const bool on = r < TB * G && i < tok1;
+    const int64_t lim = on ? limit_of(A, e, i) : 0;
+    const int step = halves ? 2 : 1;
+    float m = -INFINITY, l = 0.f;
+    int u = 0;
+#pragma unroll 1
+    for (int j = halves ? t : 0; j < nt; j += step, ++u) {
+      tc::mbar_wait(b_s + 8 * t, u & 1, abort, A.status);
+      tc::fence_after();
+      float s[BT];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, s + 32 * c);
+      tc::tmem_wait_ld();
+      const int64_t left = lim - (int64_t)(j0 + j) * BT;  // visible tokens of this tile
+      if (left < BT) {
+        const int lv = (int)max((int64_t)0, left);
+#pragma unroll
+        for (int c = 0; c < BT; ++c)
+          if (c >= lv) s[c] = -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < BT; c += 4) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mx[v] = fmaxf(mx[v], s[c + v]);
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.qscale;
+      float alpha = 1.f;
+      if (top > m + TAU) {  // also the first scores a row sees (m = -inf, alpha = 0)
+        alpha = tc::ex2(m - top);
+        m = top;
+        l *= alpha;
+      }
+      if (u > 0 && __any_sync(FULL, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tc::tmem_ld32(tO + 32 * c, o);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int v = 0; v < 32; ++v) o[v] *= alpha;
+          tc::tmem_st32(tO + 32 * c, reinterpret_cast<const uint32_t *>(o));
+        }
+        tc::tmem_wait_st();
+      }
+      const float sub = m == -INFINITY ? 0.f : -m;
+      const tc::f2 sc = tc::pack2(A.qscale, A.qscale), ms = tc::pack2(sub, sub);
+      tc::f2 sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int v = 0; v < 32; ++v) {
+          float x0, x1;
+          tc::unpack2(tc::fma2(tc::pack2(s[64 * c + 2 * v], s[64 * c + 2 * v + 1]), sc, ms), x0, x1);
+          x0 = tc::ex2(x0);
+          x1 = tc::ex2(x1);
+          sum[v & 1] = tc::add2(sum[v & 1], tc::pack2(x0, x1));
+          w[v] = tc::round2<F16>(x0, x1);
+        }
+        tc::tmem_st32(tS + 32 * c, w);
+      }
+      float l0, l1;
+      tc::unpack2(tc::add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
+      tc::tmem_wait_st();
+      tc::fence_before();
+      tc::mbar_arrive_warp(b_p + 8 * t);
+    }
+    // ---- the result: this group's m, l and accumulator
+    if (nt > 0) {
+      tc::mbar_wait(b_o, 0, abort, A.status);
+      tc::fence_after();
+    }
+    // halves: group 1 leaves its own in the stages (all consumed), group 0 joins the two
+    float *ex = reinterpret_cast<float *>(S + TILE);  // [128 rows][129], then m and l
+    const bool any1 = halves && nt > 1;
+    if (any1 && t == 1) {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tc::tmem_ld32(tO + 32 * c, o);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int v = 0; v < 32; ++v) ex[r * 129 + 32 * c + v] = o[v];
+      }
+      ex[128 * 129 + 2 * r] = m;
+      ex[128 * 129 + 2 * r + 1] = l;
+    }
+    if (any1) asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (!(halves && t == 1)) {
+      float f0 = 1.f, f1 = 0.f;
+      if (any1) {
+        const float m1 = ex[128 * 129 + 2 * r], l1 = ex[128 * 129 + 2 * r + 1];
+        const float mn = fmaxf(m, m1);
+        f0 = m == -INFINITY ? 0.f : tc::ex2(m - mn);
+        f1 = m1 == -INFINITY ? 0.f : tc::ex2(m1 - mn);
+        m = mn;
+        l = l * f0 + l1 * f1;
+      }
+      const int64_t row = (e.q0 + i) * hq + head * G + r % G;
+      const bool split = e.nsplit > 1;
+      const float inv = split ? 1.f : (l > 0.f ? 1.f / l : (l == l ? 0.f : l));
+      float *rec = split ? A.part + (e.part0 + ((int64_t)i * hq + head * G + r % G) * e.nsplit + sp) * PREC : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        if (nt > 0) {
+          tc::tmem_ld32(tO + 32 * c, o);
+          tc::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int v = 0; v < 32; ++v) o[v] = 0.f;
+        }
+        if (any1) {
+#pragma unroll
+          for (int v = 0; v < 32; ++v) o[v] = o[v] * f0 + ex[r * 129 + 32 * c + v] * f1;
+        }
+        if (on && split) {
+#pragma unroll
+          for (int v = 0; v < 32; v += 4)
+            *reinterpret_cast<float4 *>(rec + 4 + 32 * c + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
+        } else if (on) {
+          uint32_t w[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            w[v] = A.io_f16 ? tc::round2<true>(o[2 * v] * inv, o[2 * v + 1] * inv)
+                            : tc::round2<false>(o[2 * v] * inv, o[2 * v + 1] * inv);
+          uint4 *dst = reinterpret_cast<uint4 *>(A.out + row * D + 32 * c);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+        }
+      }
+      if (on && split) {
+        rec[0] = m;
+        rec[1] = l;
+      } else if (on && A.lse) {
+        A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == W_MMA) tc::tmem_free(tm, 512);
+}
+
+// Joins the splits of a row (log-sum-exp, in split order): one warp per (query token, query head).
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ BArgs A, int64_t items) {
   const int lane = threadIdx.x & 31, hq = A.hkv * A.G;
   int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (it >= items) return;
   int ei = 0;
-  while (it >= (int64_t)A.e[ei].nq * hq) it -= (int64_t)A.e[ei++].nq * hq;
-  const BEntry &e = A.e[ei];
-  const int i = (int)(it / hq), h = (int)(it % hq), head = h / A.G;
-  const int64_t row = (e.q0 + i) * hq + h;
-  const int64_t lim = A.causal ? e.n - e.nq + 1 + i : e.n;
-  float q[4], k[4], v[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  load4(A.q + row * D + 4 * lane, A.io_f16, q);
-  for (int64_t t = 0; t < lim; ++t) {
-    load4(kv_row(A, e.slot, head, 0, t) + 4 * lane, A.src.f16, k);
-    load4(kv_row(A, e.slot, head, 1, t) + 4 * lane, A.src.f16, v);
-    const float x = dot4(q, k) * A.qscale, mn = fmaxf(m, x);
-    const float a = exp2f(m - mn), p = exp2f(x - mn);
-    m = mn;
-    l = l * a + p;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = o[j] * a + p * v[j];
+  for (;; ++ei) {
+    const int64_t c = A.e[ei].nsplit > 1 ? (int64_t)A.e[ei].nq * hq : 0;
+    if (it < c) break;
+    it -= c;
   }
-  const float inv = lim > 0 ? 1.f / l : 0.f;
+  const BEntry &e = A.e[ei];
+  const float *rec = A.part + (e.part0 + it * e.nsplit) * PREC;
+  float m[2], l[2], M = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int k = lane + 32 * u;
+    m[u] = k < e.nsplit ? rec[(int64_t)k * PREC] : -INFINITY;
+    l[u] = k < e.nsplit ? rec[(int64_t)k * PREC + 1] : 0.f;
+    M = fmaxf(M, m[u]);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+  float f[2], L = 0.f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    f[u] = m[u] == -INFINITY ? 0.f : tc::ex2(m[u] - M);
+    L = fmaf(f[u], l[u], L);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < e.nsplit; ++k) {
+    const float w = __shfl_sync(FULL, (k >> 5) ? f[1] : f[0], k & 31);
+    const float4 v = *reinterpret_cast<const float4 *>(rec + (int64_t)k * PREC + 4 + 4 * lane);
+    a[0] = fmaf(w, v.x, a[0]);
+    a[1] = fmaf(w, v.y, a[1]);
+    a[2] = fmaf(w, v.z, a[2]);
+    a[3] = fmaf(w, v.w, a[3]);
+  }
+  const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+  const int64_t row = e.q0 * hq + it;
   uint2 w;
-  __nv_bfloat162 b[2] = {__floats2bfloat162_rn(o[0] * inv, o[1] * inv), __floats2bfloat162_rn(o[2] * inv, o[3] * inv)};
-  __half2 f[2] = {__floats2half2_rn(o[0] * inv, o[1] * inv), __floats2half2_rn(o[2] * inv, o[3] * inv)};
-  w = A.io_f16 ? *reinterpret_cast<const uint2 *>(f) : *reinterpret_cast<const uint2 *>(b);
+  if (A.io_f16)
+    w = make_uint2(tc::round2<true>(a[0] * inv, a[1] * inv), tc::round2<true>(a[2] * inv, a[3] * inv));
+  else
+    w = make_uint2(tc::round2<false>(a[0] * inv, a[1] * inv), tc::round2<false>(a[2] * inv, a[3] * inv));
   *reinterpret_cast<uint2 *>(A.out + row * D + 4 * lane) = w;
-  if (A.lse && lane == 0) A.lse[row] = lim > 0 ? (m + log2f(l)) / LOG2E : -INFINITY;
+  if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
 }
 
 // One warp per (token, KV head): the sum over the entry's query rows, in their order.
@@ -105,14 +549,15 @@ __global__ void __launch_bounds__(256) k_mass_rows(const __grid_constant__ BArgs
   const BEntry &e = A.e[ei];
   const int head = (int)(it / e.n);
   const int64_t t = it % e.n;
-  float q[4], k[4], sum = 0.f;
+  float q[4], k[4], kl[4], sum = 0.f;
   load4(kv_row(A, e.slot, head, 0, t) + 4 * lane, A.src.f16, k);
+  if (A.src.sides == 3) load4(kv_row(A, e.slot, head, 1, t) + 4 * lane, 1, kl);
   const int64_t i0 = A.causal ? max((int64_t)0, t - (e.n - e.nq)) : 0;
   for (int64_t r = i0 * A.G; r < (int64_t)e.nq * A.G; ++r) {
     const int64_t row = (e.q0 + r / A.G) * hq + head * A.G + r % A.G;
     load4(A.q + row * D + 4 * lane, A.io_f16, q);
     const float l = A.lse[row];
-    const float x = dot4(q, k) * A.qscale;
+    const float x = (dot4(q, k) + (A.src.sides == 3 ? dot4(q, kl) : 0.f)) * A.qscale;
     if (l != -INFINITY) sum += exp2f(x - l * LOG2E);
   }
   if (lane == 0) {
@@ -122,9 +567,9 @@ __global__ void __launch_bounds__(256) k_mass_rows(const __grid_constant__ BArgs
 }
 
 // ---- quantized caches: one side's values rebuilt in the original basis as F16 rows --------------
-// One warp per (token, head); lane holds channels 4 lane .. 4 lane + 3.  F16 keeps 11 significant
-// bits of a value of at most 8 + 11; the rounding (at most 2^-12 of the value) is the only one
-// before the products.
+// One warp per (token, head); lane holds channels 4 lane .. 4 lane + 3.  Keys are kept as an F16
+// high part and the F16 remainder (22 bits: a score is an exponent, and the log-sum-exp and the
+// weights are fp32 results); values, whose result is rounded to 16 bits, as one F16.
 struct Rebuild {
   int32_t seq, slot, which;
   int64_t n, Q;
@@ -173,9 +618,14 @@ __global__ void __launch_bounds__(256) k_rebuild(LayerView L, Rebuild R, uint16_
       for (int e = 0; e < 4; ++e) v[e] *= kKappa();
     }
   }
+  uint16_t *row = dst + ((((int64_t)R.slot * L.hkv + head) * 3 + 2 * R.which) * cap + p) * D + 4 * lane;
   const __half2 h[2] = {__floats2half2_rn(v[0], v[1]), __floats2half2_rn(v[2], v[3])};
-  *reinterpret_cast<uint2 *>(dst + ((((int64_t)R.slot * L.hkv + head) * 2 + R.which) * cap + p) * D + 4 * lane) =
-      *reinterpret_cast<const uint2 *>(h);
+  *reinterpret_cast<uint2 *>(row) = *reinterpret_cast<const uint2 *>(h);
+  if (R.which == 0) {
+    const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
+    const __half2 r[2] = {__floats2half2_rn(v[0] - a.x, v[1] - a.y), __floats2half2_rn(v[2] - b.x, v[3] - b.y)};
+    *reinterpret_cast<uint2 *>(row + cap * D) = *reinterpret_cast<const uint2 *>(r);
+  }
 }
 
 cudaError_t rebuild(int fam, int bits, const LayerView &L, const Rebuild &R, uint16_t *dst, int64_t cap,
@@ -193,20 +643,62 @@ cudaError_t rebuild(int fam, int bits, const LayerView &L, const Rebuild &R, uin
 
 // ---- host side ----------------------------------------------------------------------------------
 
-// What a call covers: its entries (those with query tokens), the sequences to rebuild.
+constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// What a call covers: its entries and the sequences to rebuild.
 struct Plan {
   std::vector<BEntry> e;
   std::vector<int> slot_seq;  // quantized cache: the sequence behind each rebuilt slot
   int64_t cap = 0;            // rows per rebuilt stream
   int64_t rows = 0;           // query tokens in all
-  size_t rebuilt_bytes = 0, bytes = 0;
+  size_t rebuilt_bytes = 0, part_bytes = 0, bytes = 0;
 };
+
+// Blocks and key splits of up to MAXE entries: without splits when there is a block for every SM;
+// otherwise the fewest key tiles per CTA (at least MIN_CPS: a join costs a launch) that one wave holds.
+void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
+  constexpr int MIN_CPS = 4;
+  const int TB = BT / G;
+  int64_t blocks = 0, most = 1;
+  for (int i = 0; i < ne; ++i) {
+    const int64_t tiles = ((int64_t)e[i].nq + TB - 1) / TB;
+    e[i].halves = tiles <= 1;
+    e[i].nblk = (int)(tiles <= 1 ? tiles : (tiles + 1) / 2);
+    blocks += (int64_t)e[i].nblk * hkv;
+    if (e[i].nblk) most = std::max(most, (e[i].n + BT - 1) / BT);
+  }
+  auto ctas = [&](int64_t cps) {
+    int64_t n = 0;
+    for (int i = 0; i < ne; ++i) n += e[i].nblk * (int64_t)hkv * std::max<int64_t>(1, ((e[i].n + BT - 1) / BT + cps - 1) / cps);
+    return n;
+  };
+  int64_t cps = most;
+  if (blocks < sms) {
+    int64_t lo = std::max<int64_t>(MIN_CPS, (most + MAXSPL - 1) / MAXSPL), hi = std::max(most, lo);
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (ctas(mid) <= sms) hi = mid; else lo = mid + 1;
+    }
+    cps = lo;
+  }
+  for (int i = 0; i < ne; ++i) {
+    const int64_t kt = (e[i].n + BT - 1) / BT;
+    e[i].nsplit = (int)std::max<int64_t>(1, (kt + cps - 1) / cps);
+    // as even as the count allows
+    e[i].cps = (int)std::max<int64_t>(1, (kt + e[i].nsplit - 1) / e[i].nsplit);
+    if (e[i].nsplit > 1) {
+      e[i].part0 = *records;
+      *records += (int64_t)e[i].nq * hkv * G * e[i].nsplit;
+    }
+  }
+}
 
 int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids, const int32_t *n_q, int n_q_heads,
               int causal, Plan *P) {
   if (!c || layer < 0 || layer >= c->p.n_layers || n_seqs < 0 || n_q_heads < 1) return KVQ_E_INVAL;
   if (n_q_heads % c->p.n_kv_heads) return KVQ_E_INVAL;
-  if (n_q_heads / c->p.n_kv_heads > MAX_G) return KVQ_E_UNSUPPORTED;
+  const int G = n_q_heads / c->p.n_kv_heads, hkv = c->p.n_kv_heads;
+  if (G > MAX_G) return KVQ_E_UNSUPPORTED;
   if (n_seqs > 0 && (!seq_ids || !n_q)) return KVQ_E_INVAL;
   const bool quant = c->fam_k != FAM_BF16;
   std::vector<int> slot(quant ? c->p.n_seqs : 0, -1);
@@ -234,8 +726,15 @@ int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids,
     }
     P->e.push_back(e);
   }
-  P->rebuilt_bytes = (size_t)P->slot_seq.size() * c->p.n_kv_heads * 2 * P->cap * (2 * D);
-  P->bytes = P->rebuilt_bytes;
+  // the longest first: their CTAs are the ones to start early
+  std::stable_sort(P->e.begin(), P->e.end(), [](const BEntry &a, const BEntry &b) { return a.n > b.n; });
+  P->rebuilt_bytes = align256((size_t)P->slot_seq.size() * hkv * 3 * P->cap * (2 * D));
+  for (size_t base = 0; base < P->e.size(); base += MAXE) {
+    int64_t records = 0;
+    plan_attn(&P->e[base], (int)std::min<size_t>(MAXE, P->e.size() - base), hkv, G, c->num_sms, &records);
+    P->part_bytes = std::max(P->part_bytes, align256(sizeof(float) * PREC * (size_t)records));
+  }
+  P->bytes = P->rebuilt_bytes + P->part_bytes;
   return KVQ_OK;
 }
 
@@ -244,11 +743,11 @@ int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, void 
                 Source *s) {
   const LayerView L = layer_view(c, layer);
   if (c->fam_k == FAM_BF16) {
-    *s = Source{reinterpret_cast<const uint16_t *>(L.ring), L.ring_cap, L.tail_f16};
+    *s = Source{reinterpret_cast<const uint16_t *>(L.ring), L.ring_cap, c->p.n_seqs, L.tail_f16, 2};
     return KVQ_OK;
   }
   uint16_t *dst = static_cast<uint16_t *>(workspace);
-  *s = Source{dst, P.cap, 1};
+  *s = Source{dst, std::max<int64_t>(P.cap, 1), std::max(1, (int)P.slot_seq.size()), 1, 3};
   for (size_t i = 0; i < P.slot_seq.size(); ++i) {
     const int64_t n = c->len[(size_t)layer * c->p.n_seqs + P.slot_seq[i]];
     for (int which = 0; which < (values ? 2 : 1); ++which) {
@@ -261,7 +760,63 @@ int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, void 
   return KVQ_OK;
 }
 
+// cuTensorMapEncodeTiled, looked up in the driver once (the library links no driver stub)
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = reinterpret_cast<EncodeFn>(p);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+// rows of 128 16-bit channels, boxes of 64 channels x 128 rows of one stream
+int map_rows(const Source &s, int hkv, CUtensorMap *map) {
+  const EncodeFn f = encoder();
+  if (!f) return KVQ_E_CUDA;
+  const cuuint64_t dims[3] = {D, (cuuint64_t)s.cap, (cuuint64_t)s.slots * hkv * s.sides};
+  const cuuint64_t strides[2] = {2 * D, (cuuint64_t)s.cap * 2 * D};
+  const cuuint32_t box[3] = {64, BT, 1}, one[3] = {1, 1, 1};
+  return f(map, s.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+           const_cast<uint16_t *>(s.base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? KVQ_OK
+             : KVQ_E_CUDA;
+}
+
+// The dynamic shared memory of a kernel, allowed once per device.
+template <typename K>
+bool allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <bool F16>
+int run_attn(const CUtensorMap &map, const BArgs &A, unsigned ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(k_attn<F16>, ATTN_SMEM, done)) return KVQ_E_CUDA;
+  k_attn<F16><<<ctas, NT, ATTN_SMEM, st>>>(map, A);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
+  note_launches(1);
+  return KVQ_OK;
+}
 
 }  // namespace
 
@@ -291,6 +846,8 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BArgs A{};
   if (const int rc = make_source(c, layer, P, true, workspace, st, &A.src)) return rc;
+  CUtensorMap map;
+  if (const int rc = map_rows(A.src, c->p.n_kv_heads, &map)) return rc;
   A.hkv = c->p.n_kv_heads;
   A.G = n_q_heads / c->p.n_kv_heads;
   A.causal = causal;
@@ -299,15 +856,26 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   A.q = static_cast<const uint16_t *>(q);
   A.out = static_cast<uint16_t *>(out);
   A.lse = lse;
+  A.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + P.rebuilt_bytes);
+  A.status = reinterpret_cast<int32_t *>(c->base + c->off_status);
   for (size_t base = 0; base < P.e.size(); base += MAXE) {
-    A.ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
-    int64_t items = 0;
-    for (int i = 0; i < A.ne; ++i) {
-      A.e[i] = P.e[base + i];
-      items += (int64_t)A.e[i].nq * n_q_heads;
+    const int ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
+    int64_t ctas = 0, joins = 0;
+    A.ne = 0;
+    for (int i = 0; i < ne; ++i) {
+      BEntry e = P.e[base + i];
+      if (e.nq == 0) continue;
+      e.cta0 = (int)ctas;
+      ctas += (int64_t)e.nblk * A.hkv * e.nsplit;
+      if (e.nsplit > 1) joins += (int64_t)e.nq * n_q_heads;
+      A.e[A.ne++] = e;
     }
-    if (items == 0) continue;
-    k_attn_rows<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(A, items);
+    if (ctas == 0) continue;
+    if (ctas > INT32_MAX) return KVQ_E_UNSUPPORTED;
+    if (const int rc = A.src.f16 ? run_attn<true>(map, A, (unsigned)ctas, st) : run_attn<false>(map, A, (unsigned)ctas, st))
+      return rc;
+    if (joins == 0) continue;
+    k_attn_join<<<(unsigned)((joins + 7) / 8), 256, 0, st>>>(A, joins);
     if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
     note_launches(1);
   }
