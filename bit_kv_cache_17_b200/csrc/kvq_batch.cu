@@ -33,6 +33,10 @@ struct BEntry {
   int32_t halves;   // one query tile: the two softmax groups take the even and the odd key tiles
   int32_t cta0;     // first CTA
   int64_t part0;    // first partial record (nsplit > 1)
+  int32_t mgroup;   // weights: groups of key pairs per KV head,
+  int32_t mpairs;   // pairs of key tiles in each,
+  int32_t mqs, mqc; // splits of the query tiles, tiles in each
+  int64_t mpart0;   // first partial sum (mqs > 1): [split][head][n rounded up to 4]
 };
 
 // 16-bit rows: row t of (slot, head, side) at ((slot * hkv + head) * sides + side) * cap + t; K is
@@ -61,22 +65,11 @@ struct BArgs {
   BEntry e[MAXE];
 };
 
-__device__ __forceinline__ const uint16_t *kv_row(const BArgs &A, int slot, int head, int side, int64_t t) {
-  return A.src.base + ((((int64_t)slot * A.hkv + head) * A.src.sides + side) * A.src.cap + t) * D;
-}
-
 __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4]) {
   const uint2 v = *reinterpret_cast<const uint2 *>(p);
   const float2 a = ring2f(v.x, f16), b = ring2f(v.y, f16);
   x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
-__device__ __forceinline__ float dot4(const float (&a)[4], const float (&b)[4]) {
-  float s = a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-  return s;
-}
-
 // ---- attention ------------------------------------------------------------------------------------
 //
 // One CTA per (entry, KV head, block of query tokens, split of the key tiles).  A tile of 128 rows
@@ -539,31 +532,303 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ BArgs
   if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
 }
 
-// One warp per (token, KV head): the sum over the entry's query rows, in their order.
-__global__ void __launch_bounds__(256) k_mass_rows(const __grid_constant__ BArgs A, int64_t items) {
-  const int lane = threadIdx.x & 31, hq = A.hkv * A.G;
-  int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+// ---- attention weights ------------------------------------------------------------------------------
+//
+// mass[t] = sum over query rows r of 2^(x[t, r] - lse2[r]): with the lse given, one product and one
+// exponential per (token, row), no second pass.  The product is taken the other way round, S^T = K.Q^T
+// (tokens are the MMA's rows), so that a thread owns a token and its sum never leaves the thread: no
+// shuffles, no atomics, the order of the sum fixed by the tiles.
+//
+// One CTA per (entry, KV head, group of key-tile pairs, split of the query tiles): the two key tiles of
+// a pair belong to the two groups of four warps and share each query tile.  Up to three query tiles
+// stay in shared memory while the keys stream past (a window of queries: each key is read once, HBM
+// bound); more of them stream for each pair (a prompt: bound by the exponentials, 16 a cycle and SM).
+// Query tiles come by TMA as [token][head] rows of 64 channels; rows that belong to no query of the
+// entry are zeroed and their lse is +inf, so they add exactly 0.
+constexpr int NKS = 4, NQS = 3;  // key and query stages
+constexpr int OFF_MCTL = (NKS + NQS) * TILE;
+
+struct MCtl {
+  uint64_t k_full[NKS], k_empty[NKS], q_full[NQS], q_empty[NQS], s_full[4], s_empty[4], tmp, last;
+  alignas(16) float nlse[NQS][BT];  // -lse * log2(e) of the tile's rows
+  uint32_t tmem;
+  int32_t abort;
+};
+constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl) + 1024;
+static_assert(MASS_SMEM <= 232448, "shared memory per CTA");
+
+template <bool F16>
+__global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensorMap kmap,
+                                                const __grid_constant__ CUtensorMap qmap,
+                                                const __grid_constant__ BArgs A) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *S = smem_raw + (base - raw);
+  MCtl &C = *reinterpret_cast<MCtl *>(S + OFF_MCTL);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int ei = 0;
+  while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
+  const BEntry &e = A.e[ei];
+  const int G = A.G, hq = A.hkv * G, TB = BT / G;
+  const int local = blockIdx.x - e.cta0;
+  const int qs = local % e.mqs, head = local / e.mqs % A.hkv;
+  const int grp = local / e.mqs / A.hkv;  // the first keys (causal: seen by most queries) first
+  const int npair = (int)((e.n + 2 * BT - 1) / (2 * BT));
+  const int p0 = grp * e.mpairs, p1 = min(npair, p0 + e.mpairs);
+  const int nqt = (e.nq + TB - 1) / TB;
+  const int qb = min(nqt, (qs + 1) * e.mqc);
+  // first query tile of this split that sees any key of pair p
+  auto first_tile = [&](int p) -> int {
+    const int64_t i = (int64_t)p * 2 * BT - (e.n - e.nq);
+    return max(qs * e.mqc, A.causal && i > 0 ? (int)(i / TB) : 0);
+  };
+  const int f0 = first_tile(p0);
+  const bool resident = qb - f0 <= NQS;
+  const bool lo = A.src.sides == 3;
+  const uint32_t q0s = base + NKS * TILE;
+  const uint32_t cb = tc::smem_u32(&C);
+  const uint32_t b_kf = cb + (uint32_t)offsetof(MCtl, k_full), b_ke = cb + (uint32_t)offsetof(MCtl, k_empty);
+  const uint32_t b_qf = cb + (uint32_t)offsetof(MCtl, q_full), b_qe = cb + (uint32_t)offsetof(MCtl, q_empty);
+  const uint32_t b_sf = cb + (uint32_t)offsetof(MCtl, s_full), b_se = cb + (uint32_t)offsetof(MCtl, s_empty);
+  const uint32_t b_tmp = cb + (uint32_t)offsetof(MCtl, tmp), b_last = cb + (uint32_t)offsetof(MCtl, last);
+  volatile int32_t *abort = &C.abort;
+
+  if (warp == W_LOAD && lane == 0) {
+    for (int i = 0; i < NKS; ++i) {
+      tc::mbar_init(b_kf + 8 * i, 1);
+      tc::mbar_init(b_ke + 8 * i, 1);
+    }
+    for (int i = 0; i < NQS; ++i) {
+      tc::mbar_init(b_qf + 8 * i, 2);           // the copy, and the lse values
+      tc::mbar_init(b_qe + 8 * i, 1 + NSOFT);   // the products, and the softmax warps
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(b_sf + 8 * i, 1);
+      tc::mbar_init(b_se + 8 * i, 4);
+    }
+    tc::mbar_init(b_tmp, 1);
+    tc::mbar_init(b_last, 1);
+    C.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == W_MMA) tc::tmem_alloc(cb + (uint32_t)offsetof(MCtl, tmem), 512);
+  // rows of the query stages that no copy writes
+  for (int u = tid; u < NQS * (BT - TB * G) * 16; u += NT) {
+    const int st = u / ((BT - TB * G) * 16), v = u % ((BT - TB * G) * 16);
+    *reinterpret_cast<uint4 *>(S + (NKS + st) * TILE + (v & 1) * HALF + (TB * G + (v >> 4)) * 128 + ((v >> 1) & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  tc::fence_async_smem();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = C.tmem;
+  const int z0 = (e.slot * A.hkv + head) * A.src.sides;
+
+  if (warp == W_LOAD) {
+    int kc = 0, qc = 0, patched = 0;
+    auto load_k = [&](int64_t t0, int z) {
+      const int st = kc % NKS;
+      if (kc >= NKS) tc::mbar_wait(b_ke + 8 * st, (kc / NKS - 1) & 1, abort, A.status);
+      if (lane == 0) {
+        tc::mbar_expect(b_kf + 8 * st, TILE);
+        tc::tma_load3(base + st * TILE, &kmap, 0, (int)t0, z, b_kf + 8 * st);
+        tc::tma_load3(base + st * TILE + HALF, &kmap, 64, (int)t0, z, b_kf + 8 * st);
+      }
+      __syncwarp();
+      ++kc;
+    };
+    auto load_q = [&](int a) {
+      const int st = qc % NQS;
+      if (qc >= NQS) tc::mbar_wait(b_qe + 8 * st, (qc / NQS - 1) & 1, abort, A.status);
+      const int nc = min(TB, e.nq - a * TB) * G;
+      const bool patch = nc < TB * G;  // other entries' rows, or none, behind this entry's last
+      const uint32_t bar = patch ? b_tmp : b_qf + 8 * st, dst = q0s + st * TILE;
+      if (lane == 0) {
+        tc::mbar_expect(bar, 2 * TB * G * 128);
+        tc::tma_load4(dst, &qmap, 0, 0, head, (int)(e.q0 + a * TB), bar);
+        tc::tma_load4(dst + HALF, &qmap, 64, 0, head, (int)(e.q0 + a * TB), bar);
+      }
+      for (int c = lane; c < BT; c += 32) {
+        float v = -INFINITY;
+        if (c < nc) {
+          v = __ldg(A.lse + (e.q0 + a * TB + c / G) * hq + head * G + c % G);
+          v = v == -INFINITY ? v : -v * LOG2E;
+        }
+        C.nlse[st][c] = v;
+      }
+      if (patch) {
+        tc::mbar_wait(b_tmp, patched & 1, abort, A.status, false);
+        ++patched;
+        for (int u = lane; u < (TB * G - nc) * 16; u += 32)
+          *reinterpret_cast<uint4 *>(S + (NKS + st) * TILE + (u & 1) * HALF + (nc + (u >> 4)) * 128 + ((u >> 1) & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_async_smem();
+        tc::mbar_arrive_warp(b_qf + 8 * st);
+      }
+      tc::mbar_arrive_warp(b_qf + 8 * st);
+      ++qc;
+    };
+#pragma unroll 1
+    for (int p = p0; p < p1; ++p) {
+      const int f = first_tile(p);
+      if (f >= qb) break;  // (the keys behind see fewer queries still)
+      const int64_t key0 = (int64_t)p * 2 * BT;
+      for (int t = 0; t < 2 && key0 + t * BT < e.n; ++t) {
+        load_k(key0 + t * BT, z0);
+        if (lo) load_k(key0 + t * BT, z0 + 1);
+      }
+      if (!resident || p == p0)
+        for (int a = f; a < qb; ++a) load_q(a);
+    }
+    for (int i = max(0, kc - NKS); i < kc; ++i)
+      tc::mbar_wait(b_kf + 8 * (i % NKS), (i / NKS) & 1, abort, A.status, false);
+    for (int i = max(0, qc - NQS); i < qc; ++i)
+      tc::mbar_wait(b_qf + 8 * (i % NQS), (i / NQS) & 1, abort, A.status, false);
+  } else if (warp == W_MMA) {
+    if (lane == 0) {
+      constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0);
+      int kc = 0, qc = 0, sc[2] = {0, 0};
+#pragma unroll 1
+      for (int p = p0; p < p1; ++p) {
+        const int f = first_tile(p);
+        if (f >= qb) break;
+        const int nk = (int64_t)p * 2 * BT + BT < e.n ? 2 : 1, per = lo ? 2 : 1;
+        for (int u = 0; u < nk * per; ++u)
+          tc::mbar_wait(b_kf + 8 * ((kc + u) % NKS), ((kc + u) / NKS) & 1, abort, A.status);
+#pragma unroll 1
+        for (int a = f; a < qb; ++a) {
+          const int qi = resident ? a - f0 : qc++, st = qi % NQS;
+          tc::mbar_wait(b_qf + 8 * st, (qi / NQS) & 1, abort, A.status);
+          tc::fence_after();
+          const uint64_t q = tc::desc_sw128(q0s + st * TILE, 0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= nk) break;
+            const int b = 2 * t + (sc[t] & 1);
+            if (sc[t] >= 2) {
+              tc::mbar_wait(b_se + 8 * b, (sc[t] / 2 - 1) & 1, abort, A.status);
+              tc::fence_after();
+            }
+            for (int h = 0; h < per; ++h) {
+              const uint64_t k = tc::desc_sw128(base + ((kc + t * per + h) % NKS) * TILE, 0);
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s) {
+                const uint64_t o = (uint64_t)((s & 3) * 2 + (s >> 2) * (HALF >> 4));
+                tc::mma_ss(tm + BT * b, k + o, q + o, idS, h == 0 && s == 0 ? 0u : 1u);
+              }
+            }
+            tc::commit(b_sf + 8 * b);
+            ++sc[t];
+          }
+          if (!resident) tc::commit(b_qe + 8 * st);
+        }
+        for (int u = 0; u < nk * per; ++u) tc::commit(b_ke + 8 * ((kc + u) % NKS));
+        kc += nk * per;
+      }
+      tc::commit(b_last);
+      tc::mbar_wait(b_last, 0, abort, A.status, false);
+    }
+    __syncwarp();
+  } else {
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const tc::f2 sc2 = tc::pack2(A.qscale, A.qscale);
+    int qc = 0, sc = 0;
+#pragma unroll 1
+    for (int p = p0; p < p1; ++p) {
+      const int f = first_tile(p);
+      const int64_t tile0 = (int64_t)p * 2 * BT + t * BT, key = tile0 + r;
+      float total = 0.f, rest = 0.f;  // the sum over query tiles and what its additions rounded off
+#pragma unroll 1
+      for (int a = f; a < qb; ++a) {
+        const int qi = resident ? a - f0 : qc++, st = qi % NQS;
+        tc::mbar_wait(b_qf + 8 * st, (qi / NQS) & 1, abort, A.status);
+        if (tile0 < e.n) {
+          const int b = 2 * t + (sc & 1);
+          tc::mbar_wait(b_sf + 8 * b, (sc / 2) & 1, abort, A.status);
+          ++sc;
+          tc::fence_after();
+          const uint32_t tS = tm + lanes + BT * b;
+          // columns below c0 are queries in front of the token (causal)
+          const int64_t hid = A.causal ? (key - (e.n - e.nq) - (int64_t)a * TB) * G : 0;
+          const int c0 = (int)max((int64_t)0, min((int64_t)BT, hid));
+          const bool masked = __any_sync(FULL, c0 > 0);
+          tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float s[64];
+            tc::tmem_ld32(tS + 64 * h, s);
+            tc::tmem_ld32(tS + 64 * h + 32, s + 32);
+            tc::tmem_wait_ld();
+            if (h == 1) {
+              tc::fence_before();
+              tc::mbar_arrive_warp(b_se + 8 * b);
+            }
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (64 * h + c < c0) s[c] = -INFINITY;
+            }
+            const float4 *nl = reinterpret_cast<const float4 *>(&C.nlse[st][64 * h]);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float4 n4 = nl[c];
+              float x0, x1, x2, x3;
+              tc::unpack2(tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y)), x0, x1);
+              tc::unpack2(tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w)), x2, x3);
+              sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(tc::ex2(x0), tc::ex2(x1)));
+              sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
+            }
+          }
+          float v0, v1;
+          tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), v0, v1);
+          const float v = v0 + v1, n = total + v, d = n - total;
+          rest += (total - (n - d)) + (v - d);
+          total = n;
+        }
+        if (!resident) tc::mbar_arrive_warp(b_qe + 8 * st);
+      }
+      if (key < e.n) {
+        const float v = total + rest;
+        if (e.mqs > 1) {
+          A.part[e.mpart0 + ((int64_t)qs * A.hkv + head) * ((e.n + 3) & ~3ll) + key] = v;
+        } else {
+          const int64_t at = ((int64_t)e.out * A.hkv + head) * A.mass_ld + key;
+          A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == W_MMA) tc::tmem_free(tm, 512);
+}
+
+// Adds the splits of the query tiles, in order: one thread per (token, KV head).
+__global__ void __launch_bounds__(256) k_mass_join(const __grid_constant__ BArgs A, int64_t items) {
+  int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (it >= items) return;
   int ei = 0;
-  while (it >= A.e[ei].n * A.hkv) it -= A.e[ei++].n * A.hkv;
+  for (;; ++ei) {
+    const int64_t c = A.e[ei].mqs > 1 ? A.e[ei].n * A.hkv : 0;
+    if (it < c) break;
+    it -= c;
+  }
   const BEntry &e = A.e[ei];
-  const int head = (int)(it / e.n);
-  const int64_t t = it % e.n;
-  float q[4], k[4], kl[4], sum = 0.f;
-  load4(kv_row(A, e.slot, head, 0, t) + 4 * lane, A.src.f16, k);
-  if (A.src.sides == 3) load4(kv_row(A, e.slot, head, 1, t) + 4 * lane, 1, kl);
-  const int64_t i0 = A.causal ? max((int64_t)0, t - (e.n - e.nq)) : 0;
-  for (int64_t r = i0 * A.G; r < (int64_t)e.nq * A.G; ++r) {
-    const int64_t row = (e.q0 + r / A.G) * hq + head * A.G + r % A.G;
-    load4(A.q + row * D + 4 * lane, A.io_f16, q);
-    const float l = A.lse[row];
-    const float x = (dot4(q, k) + (A.src.sides == 3 ? dot4(q, kl) : 0.f)) * A.qscale;
-    if (l != -INFINITY) sum += exp2f(x - l * LOG2E);
-  }
-  if (lane == 0) {
-    const int64_t at = ((int64_t)e.out * A.hkv + head) * A.mass_ld + t;
-    A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + sum : sum;
-  }
+  const int64_t head = it / e.n, t = it % e.n, ld = (e.n + 3) & ~3ll;
+  float v = 0.f;
+  for (int k = 0; k < e.mqs; ++k) v += A.part[e.mpart0 + (k * A.hkv + head) * ld + t];
+  const int64_t at = ((int64_t)e.out * A.hkv + head) * A.mass_ld + t;
+  A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
+}
+
+// BF16 queries as F16 rows, for the products with a rebuilt cache (exact in the F16 range)
+__global__ void __launch_bounds__(256) k_q16(const uint4 *q, uint4 *dst, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) dst[i] = bf16x8_to_ring(q[i], 1);
 }
 
 // ---- quantized caches: one side's values rebuilt in the original basis as F16 rows --------------
@@ -651,7 +916,7 @@ struct Plan {
   std::vector<int> slot_seq;  // quantized cache: the sequence behind each rebuilt slot
   int64_t cap = 0;            // rows per rebuilt stream
   int64_t rows = 0;           // query tokens in all
-  size_t rebuilt_bytes = 0, part_bytes = 0, bytes = 0;
+  size_t rebuilt_bytes = 0, part_bytes = 0, q16_bytes = 0, bytes = 0;
 };
 
 // Blocks and key splits of up to MAXE entries: without splits when there is a block for every SM;
@@ -693,6 +958,40 @@ void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
   }
 }
 
+// Groups of key pairs and splits of the query tiles.  Up to three query tiles: they stay in shared
+// memory, and one wave of CTAs streams the keys.  More: items of about an eighth of an SM's share,
+// so that the causal ones even out.
+void plan_mass(BEntry *e, int ne, int hkv, int G, int sms, int64_t *floats) {
+  const int TB = BT / G;
+  int64_t units = 0, most = 1;
+  bool heavy = false;
+  for (int i = 0; i < ne; ++i) {
+    const int64_t np = (e[i].n + 2 * BT - 1) / (2 * BT), qt = ((int64_t)e[i].nq + TB - 1) / TB;
+    units += hkv * np * std::max<int64_t>(1, qt);
+    most = std::max(most, np);
+    heavy |= qt > NQS;
+  }
+  const int64_t target = std::min<int64_t>(64, std::max<int64_t>(8, units / (8 * sms)));
+  int64_t lo = 1, hi = most;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    int64_t n = 0;
+    for (int i = 0; i < ne; ++i) n += hkv * (((e[i].n + 2 * BT - 1) / (2 * BT) + mid - 1) / mid);
+    if (n <= sms) hi = mid; else lo = mid + 1;
+  }
+  for (int i = 0; i < ne; ++i) {
+    const int64_t np = (e[i].n + 2 * BT - 1) / (2 * BT), qt = std::max<int64_t>(1, ((int64_t)e[i].nq + TB - 1) / TB);
+    e[i].mqs = heavy ? (int)((qt + target - 1) / target) : 1;
+    e[i].mqc = (int)((qt + e[i].mqs - 1) / e[i].mqs);
+    e[i].mpairs = (int)(heavy ? std::max<int64_t>(1, std::min(np, target / qt)) : lo);
+    e[i].mgroup = (int)((np + e[i].mpairs - 1) / e[i].mpairs);
+    if (e[i].mqs > 1) {
+      e[i].mpart0 = *floats;
+      *floats += (int64_t)e[i].mqs * hkv * ((e[i].n + 3) & ~3ll);
+    }
+  }
+}
+
 int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids, const int32_t *n_q, int n_q_heads,
               int causal, Plan *P) {
   if (!c || layer < 0 || layer >= c->p.n_layers || n_seqs < 0 || n_q_heads < 1) return KVQ_E_INVAL;
@@ -726,15 +1025,20 @@ int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids,
     }
     P->e.push_back(e);
   }
+  if (P->rows > INT32_MAX) return KVQ_E_UNSUPPORTED;
   // the longest first: their CTAs are the ones to start early
   std::stable_sort(P->e.begin(), P->e.end(), [](const BEntry &a, const BEntry &b) { return a.n > b.n; });
   P->rebuilt_bytes = align256((size_t)P->slot_seq.size() * hkv * 3 * P->cap * (2 * D));
   for (size_t base = 0; base < P->e.size(); base += MAXE) {
-    int64_t records = 0;
-    plan_attn(&P->e[base], (int)std::min<size_t>(MAXE, P->e.size() - base), hkv, G, c->num_sms, &records);
-    P->part_bytes = std::max(P->part_bytes, align256(sizeof(float) * PREC * (size_t)records));
+    int64_t records = 0, floats = 0;
+    const int ne = (int)std::min<size_t>(MAXE, P->e.size() - base);
+    plan_attn(&P->e[base], ne, hkv, G, c->num_sms, &records);
+    plan_mass(&P->e[base], ne, hkv, G, c->num_sms, &floats);
+    P->part_bytes = std::max({P->part_bytes, align256(sizeof(float) * PREC * (size_t)records),
+                              align256(sizeof(float) * (size_t)floats)});
   }
-  P->bytes = P->rebuilt_bytes + P->part_bytes;
+  if (quant && !c->p.tail_f16) P->q16_bytes = align256((size_t)P->rows * n_q_heads * 2 * D);
+  P->bytes = P->rebuilt_bytes + P->part_bytes + P->q16_bytes;
   return KVQ_OK;
 }
 
@@ -794,6 +1098,20 @@ int map_rows(const Source &s, int hkv, CUtensorMap *map) {
              : KVQ_E_CUDA;
 }
 
+// query rows as [token][KV head][G][128], boxes of 64 channels x the G heads x as many tokens as fill a tile
+int map_queries(const void *q, int f16, int hkv, int G, int64_t rows, CUtensorMap *map) {
+  const EncodeFn f = encoder();
+  if (!f) return KVQ_E_CUDA;
+  const cuuint64_t dims[4] = {D, (cuuint64_t)G, (cuuint64_t)hkv, (cuuint64_t)rows};
+  const cuuint64_t strides[3] = {2 * D, (cuuint64_t)G * 2 * D, (cuuint64_t)hkv * G * 2 * D};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)(BT / G)}, one[4] = {1, 1, 1, 1};
+  return f(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q),
+           dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? KVQ_OK
+             : KVQ_E_CUDA;
+}
+
 // The dynamic shared memory of a kernel, allowed once per device.
 template <typename K>
 bool allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done) {
@@ -813,6 +1131,16 @@ int run_attn(const CUtensorMap &map, const BArgs &A, unsigned ctas, cudaStream_t
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(k_attn<F16>, ATTN_SMEM, done)) return KVQ_E_CUDA;
   k_attn<F16><<<ctas, NT, ATTN_SMEM, st>>>(map, A);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
+  note_launches(1);
+  return KVQ_OK;
+}
+
+template <bool F16>
+int run_mass(const CUtensorMap &kmap, const CUtensorMap &qmap, const BArgs &A, unsigned ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(k_mass<F16>, MASS_SMEM, done)) return KVQ_E_CUDA;
+  k_mass<F16><<<ctas, NT, MASS_SMEM, st>>>(kmap, qmap, A);
   if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
   note_launches(1);
   return KVQ_OK;
@@ -916,15 +1244,41 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   A.mass_out = mass_out;
   A.mass_ld = mass_ld;
   A.decay = decay;
-  for (size_t base = 0; base < P.e.size(); base += MAXE) {
-    A.ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
-    int64_t items = 0;
-    for (int i = 0; i < A.ne; ++i) {
-      A.e[i] = P.e[base + i];
-      items += A.e[i].n * A.hkv;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  A.part = reinterpret_cast<float *>(ws + P.rebuilt_bytes);
+  A.status = reinterpret_cast<int32_t *>(c->base + c->off_status);
+  CUtensorMap kmap, qmap{};
+  if (const int rc = map_rows(A.src, A.hkv, &kmap)) return rc;
+  if (P.rows > 0) {
+    if (P.q16_bytes) {
+      uint4 *q16 = reinterpret_cast<uint4 *>(ws + P.rebuilt_bytes + P.part_bytes);
+      const int64_t n = P.rows * n_q_heads * (D / 8);
+      k_q16<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(static_cast<const uint4 *>(q), q16, n);
+      if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
+      note_launches(1);
+      q = q16;
     }
-    if (items == 0) continue;
-    k_mass_rows<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(A, items);
+    if (const int rc = map_queries(q, A.src.f16, A.hkv, A.G, P.rows, &qmap)) return rc;
+  }
+  for (size_t base = 0; base < P.e.size(); base += MAXE) {
+    const int ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
+    int64_t ctas = 0, joins = 0;
+    A.ne = 0;
+    for (int i = 0; i < ne; ++i) {
+      BEntry e = P.e[base + i];
+      if (e.n == 0) continue;
+      e.cta0 = (int)ctas;
+      ctas += (int64_t)e.mgroup * A.hkv * e.mqs;
+      if (e.mqs > 1) joins += e.n * A.hkv;
+      A.e[A.ne++] = e;
+    }
+    if (ctas == 0) continue;
+    if (ctas > INT32_MAX) return KVQ_E_UNSUPPORTED;
+    if (const int rc = A.src.f16 ? run_mass<true>(kmap, qmap, A, (unsigned)ctas, st)
+                                 : run_mass<false>(kmap, qmap, A, (unsigned)ctas, st))
+      return rc;
+    if (joins == 0) continue;
+    k_mass_join<<<(unsigned)((joins + 255) / 256), 256, 0, st>>>(A, joins);
     if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
     note_launches(1);
   }

@@ -72,6 +72,14 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle (tiles as TMA writes them: rows of 128 bytes,
 // 1024-byte aligned groups of 8).  K-major operand: lbo unused, sbo = 1024 (8 rows).  MN-major
 // operand: lbo = the distance of the next 64 elements, sbo = 1024 (8 rows along K).
