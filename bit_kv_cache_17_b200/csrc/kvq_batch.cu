@@ -18,7 +18,7 @@ using namespace kvq;
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int MAXE = 64;  // entries per launch
+constexpr int MAXE = 32;  // entries per launch (kernel arguments of 4 KB)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -1001,6 +1001,7 @@ int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids,
   if (n_seqs > 0 && (!seq_ids || !n_q)) return KVQ_E_INVAL;
   const bool quant = c->fam_k != FAM_BF16;
   std::vector<int> slot(quant ? c->p.n_seqs : 0, -1);
+  P->e.reserve(n_seqs);
   for (int i = 0; i < n_seqs; ++i) {
     const int s = seq_ids[i];
     if (s < 0 || s >= c->p.n_seqs || n_q[i] < 0) return KVQ_E_INVAL;

@@ -261,36 +261,32 @@ def kvq_describe(h):
     return _lib.kvq_describe(h).decode()
 
 
-def _refuse(cond, where, why, code=KVQ_E_INVAL):
-    if cond:
-        raise KVQError(code, f"{where}: {why}")
+def _refuse(where, why, code=KVQ_E_INVAL):
+    raise KVQError(code, f"{where}: {why}")
 
 
-class _Call:
-    """Where a call's tensors are made and its kernels run: `stream` (a torch stream, or the
-    device's current one).  Outputs and workspace come from the caching allocator under that
-    stream, so calls on several streams, and captured graphs, each have their own."""
+def _raw_stream_of(torch):
+    """device index -> the cudaStream_t current on it (the same number as
+    torch.cuda.current_stream(index).cuda_stream, without building the stream object)"""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
 
-    __slots__ = ("torch", "device", "stream", "inner", "outer")
+
+class _On:
+    """Makes a device and a stream current: outputs and workspace then come from the caching
+    allocator under the stream the kernels run on, so calls on several streams, and captured graphs,
+    each have their own."""
 
     def __init__(self, torch, device, stream):
-        self.torch, self.device = torch, device
-        self.outer = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.inner = None if stream is None else torch.cuda.stream(stream)
+        self.both = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
-        if self.outer is not None:
-            self.outer.__enter__()
-        if self.inner is not None:
-            self.inner.__enter__()
-        return self.stream.cuda_stream
+        for c in self.both:
+            c.__enter__()
 
     def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-        if self.outer is not None:
-            self.outer.__exit__(*exc)
+        for c in reversed(self.both):
+            c.__exit__(*exc)
 
 
 class Rope:
@@ -306,27 +302,35 @@ class Rope:
 
         self.torch = torch
         sections = [int(x) for x in sections]
-        _refuse(not 1 <= len(sections) <= 4, "Rope", "1 to 4 sections")
+        if not 1 <= len(sections) <= 4:
+            _refuse("Rope", "1 to 4 sections")
         rot_dim = 2 * sum(sections) if rot_dim is None else int(rot_dim)
         self.n_axes = len(sections)
         self._p = [kvq_rope_default_params(rot_dim=rot_dim, n_axes=self.n_axes,
                                            sections=sections + [0] * (4 - len(sections)), turns=int(turns),
                                            adjacent=int(adjacent), inverse=i, theta=float(theta)) for i in (0, 1)]
+        self._ref = [C.byref(p) for p in self._p]
         self._freq = None
         if inv_freq is not None:
             f = [float(x) for x in inv_freq]
-            _refuse(len(f) != rot_dim // 2, "Rope", "inv_freq holds rot_dim / 2 values")
+            if len(f) != rot_dim // 2:
+                _refuse("Rope", "inv_freq holds rot_dim / 2 values")
             self._freq = (C.c_double * len(f))(*f)
+        self._raw_stream = _raw_stream_of(torch)
         self._types = {torch.float32: KVQ_DT_F32, torch.bfloat16: KVQ_DT_BF16, torch.float16: KVQ_DT_F16}
         # the host checks of the parameters, once: a call over no tokens
         kvq_rope(self._p[0], self._freq, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
 
-    def _rows(self, x, n, name):
-        _refuse(x.dim() != 3 or x.shape[0] != n or x.shape[2] != 128 or x.stride(2) != 1 or
-                (x.shape[1] > 1 and x.stride(1) != 128), "Rope.apply",
-                f"{name} is [tokens, heads, 128] with contiguous heads")
-        # the row stride of a single token says nothing
-        return x.stride(0) if n > 1 else max(x.stride(0), x.shape[1] * 128)
+    @staticmethod
+    def _rows(x, n, dev, name):
+        """(heads, pointer, row stride) of a [tokens, heads, 128] tensor with contiguous heads"""
+        s, st = x.shape, x.stride()
+        if len(s) != 3 or s[0] != n or s[2] != 128 or st[2] != 1 or (s[1] > 1 and st[1] != 128):
+            _refuse("Rope.apply", f"{name} is [tokens, heads, 128] with contiguous heads")
+        if x.get_device() != dev:
+            _refuse("Rope.apply", f"{name} is on another device than pos")
+        # (the row stride of a single token says nothing)
+        return s[1], x.data_ptr(), st[0] if n > 1 else max(st[0], s[1] * 128)
 
     def apply(self, pos, q=None, k=None, q_dtype=None, inverse=False, q_out=None, k_out=None, stream=None):
         """pos: int32 [n_axes, tokens] (or [tokens] for one axis); q: [tokens, heads, 128] fp32, BF16
@@ -334,35 +338,49 @@ class Rope:
         contiguous tensors (q of q_dtype, its own type by default) unless given; an output may be its
         input."""
         torch = self.torch
-        if pos.dim() == 1:
-            pos = pos[None]
-        _refuse(pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[0] != self.n_axes, "Rope.apply",
-                "pos is int32 [n_axes, tokens]")
-        n = pos.shape[1]
-        _refuse(n > 1 and pos.stride(1) != 1, "Rope.apply", "the tokens of pos are contiguous")
-        pos_ld = pos.stride(0) if self.n_axes > 1 else n
-        for x in (q, k, q_out, k_out):
-            _refuse(x is not None and x.device != pos.device, "Rope.apply", "tensors on different devices")
-        _refuse(pos.device.type != "cuda", "Rope.apply", "tensors are on a CUDA device")
-        with _Call(torch, pos.device, stream) as st:
-            a, b = (0, 0, 0, 0, 0, 0, 0), (0, 0, 0, 0, 0)
-            if q is not None:
-                if q_out is None:
-                    q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
-                _refuse(q.dtype not in self._types or q_out.dtype not in self._types or
-                        (q_dtype is not None and q_out.dtype != q_dtype), "Rope.apply", "type of q",
-                        KVQ_E_UNSUPPORTED)
-                _refuse(q_out.shape != q.shape, "Rope.apply", "q_out has q's shape")
-                a = (q.shape[1], q.data_ptr(), self._types[q.dtype], self._rows(q, n, "q"), q_out.data_ptr(),
-                     self._types[q_out.dtype], self._rows(q_out, n, "q_out"))
-            if k is not None:
-                if k_out is None:
-                    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-                _refuse(k.dtype != torch.bfloat16 or k_out.dtype != torch.bfloat16, "Rope.apply", "k is BF16",
-                        KVQ_E_UNSUPPORTED)
-                _refuse(k_out.shape != k.shape, "Rope.apply", "k_out has k's shape")
-                b = (k.shape[1], k.data_ptr(), self._rows(k, n, "k"), k_out.data_ptr(), self._rows(k_out, n, "k_out"))
-            kvq_rope(self._p[int(bool(inverse))], self._freq, n, pos.data_ptr(), max(pos_ld, n), *a, *b, st)
+        dev = pos.get_device()
+        if dev < 0:
+            _refuse("Rope.apply", "tensors are on a CUDA device")
+        if stream is not None or torch.cuda.current_device() != dev:
+            with _On(torch, pos.device, stream):
+                return self.apply(pos, q, k, q_dtype, inverse, q_out, k_out)
+        shape = pos.shape
+        if len(shape) == 1:
+            pos, shape = pos[None], (1, shape[0])
+        n = shape[1]
+        if pos.dtype is not torch.int32 or len(shape) != 2 or shape[0] != self.n_axes or (n > 1 and pos.stride(1) != 1):
+            _refuse("Rope.apply", "pos is int32 [n_axes, tokens], the tokens contiguous")
+        pos_ld = max(pos.stride(0), n) if self.n_axes > 1 else n
+        a, b = (0, 0, 0, 0, 0, 0, 0), (0, 0, 0, 0, 0)
+        if q is not None:
+            h, ptr, ld = self._rows(q, n, dev, "q")
+            if q_out is None:
+                q_out = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
+                ho, ptr_o, ld_o = h, q_out.data_ptr(), h * 128
+            else:
+                ho, ptr_o, ld_o = self._rows(q_out, n, dev, "q_out")
+            ti, to = self._types.get(q.dtype), self._types.get(q_out.dtype)
+            if ti is None or to is None or (q_dtype is not None and q_out.dtype is not q_dtype):
+                _refuse("Rope.apply", "type of q", KVQ_E_UNSUPPORTED)
+            if ho != h:
+                _refuse("Rope.apply", "q_out has q's heads")
+            a = (h, ptr, ti, ld, ptr_o, to, ld_o)
+        if k is not None:
+            h, ptr, ld = self._rows(k, n, dev, "k")
+            if k_out is None:
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+                ho, ptr_o, ld_o = h, k_out.data_ptr(), h * 128
+            else:
+                ho, ptr_o, ld_o = self._rows(k_out, n, dev, "k_out")
+            if k.dtype is not torch.bfloat16 or k_out.dtype is not torch.bfloat16:
+                _refuse("Rope.apply", "k is BF16", KVQ_E_UNSUPPORTED)
+            if ho != h:
+                _refuse("Rope.apply", "k_out has k's heads")
+            b = (h, ptr, ld, ptr_o, ld_o)
+        rc = _lib.kvq_rope(self._ref[1 if inverse else 0], self._freq, n, pos.data_ptr(), pos_ld, *a, *b,
+                           self._raw_stream(dev))
+        if rc:
+            raise KVQError(rc, "kvq_rope")
         return q_out, k_out
 
 
@@ -383,6 +401,11 @@ class KVCache:
         self.storage = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             self.handle = kvq_cache_create(self.params, self.storage.data_ptr(), self.nbytes)
+        self._index = self.storage.get_device()
+        self._t16 = torch.float16 if self.params.tail_f16 else torch.bfloat16
+        self._raw_stream = _raw_stream_of(torch)
+        self._size = _sz()
+        self._size_ref = C.byref(self._size)
         self._ws = None
         self._ws_bytes = {}  # (n_seqs, n_q_heads) -> kvq_workspace_bytes
 
@@ -453,22 +476,52 @@ class KVCache:
         torch, p = self.torch, self.params
         kvarn = any(8 <= t <= 13 or (p.var_norm and t != 0) for t in (p.type_k, p.type_v))
         rows = p.max_ctx if p.type_k == 0 else p.tail + (256 if kvarn else 0)
-        _refuse(rows == 0, "rows16", "a cache without a 16-bit tail")
+        if rows == 0:
+            _refuse("rows16", "a cache without a 16-bit tail")
         off, _ = kvq_locate(self.handle, 1, layer, 0, 0, 0, 0, 0)
         n = p.n_seqs * p.n_kv_heads * 2 * rows * 128
         x = self.storage[off:off + 2 * n].view(torch.float16 if p.tail_f16 else torch.bfloat16)
         return x.view(p.n_seqs, p.n_kv_heads, 2, rows, 128)
 
-    def _same_device(self, x, where, name):
-        _refuse(x.device != self.storage.device, where, f"{name} is on another device than the cache")
+    def _elsewhere(self, stream):
+        """Whether a stream or device other than the current one has to be made current (_on)."""
+        return stream is not None or self.torch.cuda.current_device() != self._index
+
+    def _on(self, stream):
+        return _On(self.torch, self.storage.device, stream)
 
     def _queries(self, where, q, n_q):
-        torch = self.torch
-        _refuse(q.dtype != (torch.float16 if self.params.tail_f16 else torch.bfloat16), where,
-                "q is in the cache's 16-bit type (BF16, or F16 with tail_f16)", KVQ_E_UNSUPPORTED)
-        _refuse(q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous() or q.shape[0] != sum(n_q), where,
-                "q is contiguous [sum(n_q), n_q_heads, 128]")
-        self._same_device(q, where, "q")
+        s = q.shape
+        if q.dtype is not self._t16:
+            _refuse(where, "q is in the cache's 16-bit type (BF16, or F16 with tail_f16)", KVQ_E_UNSUPPORTED)
+        if len(s) != 3 or s[2] != 128 or s[0] != sum(n_q) or not q.is_contiguous():
+            _refuse(where, "q is contiguous [sum(n_q), n_q_heads, 128]")
+        if q.get_device() != self._index:
+            _refuse(where, "q is on another device than the cache")
+        return s[0], s[1]
+
+    def _lse(self, where, lse, rows, hq):
+        if lse.dtype is not self.torch.float32 or lse.shape != (rows, hq) or not lse.is_contiguous() or \
+                lse.get_device() != self._index:
+            _refuse(where, "lse is contiguous fp32 [sum(n_q), n_q_heads] on the cache's device")
+
+    def _mass_rows(self, where, x, n, name):
+        s = x.shape
+        if x.dtype is not self.torch.float32 or len(s) != 3 or s[0] != n or s[1] != self.params.n_kv_heads or \
+                not x.is_contiguous() or x.get_device() != self._index:
+            _refuse(where, f"{name} is contiguous fp32 [sequences, n_kv_heads, tokens] on the cache's device")
+        return s[2]
+
+    def _batch_workspace(self, layer, n, ids, nq, hq):
+        """(the tensor that owns it or None, pointer, bytes)"""
+        rc = _lib.kvq_batch_workspace_bytes(self.handle, layer, n, ids, nq, hq, self._size_ref)
+        if rc:
+            raise KVQError(rc, "kvq_batch_workspace_bytes")
+        nb = self._size.value
+        if nb == 0:
+            return None, 0, 0
+        ws = self.torch.empty(nb, dtype=self.torch.uint8, device=self.storage.device)
+        return ws, ws.data_ptr(), nb
 
     def batch_attn(self, layer, seq_ids, n_q, q, causal=False, out=None, lse=None, return_lse=False, softmax_scale=0.0,
                    stream=None):
@@ -476,36 +529,30 @@ class KVCache:
         over sequence seq_ids[i]; every token seen (cross attention), or causal over the newest n_q[i].
         Returns out, or (out, lse [sum(n_q), n_q_heads] fp32) with return_lse or a given lse."""
         torch = self.torch
-        seq_ids, n_q = list(seq_ids), list(n_q)
-        _refuse(len(seq_ids) != len(n_q), "batch_attn", "one n_q for each sequence")
-        self._queries("batch_attn", q, n_q)
-        hq = q.shape[1]
-        with _Call(torch, self.storage.device, stream) as st:
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None and return_lse:
-                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-            _refuse(out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous(), "batch_attn",
-                    "out has q's shape and type")
-            self._same_device(out, "batch_attn", "out")
-            if lse is not None:
-                self._lse("batch_attn", lse, q)
-            nb = kvq_batch_workspace_bytes(self.handle, layer, seq_ids, n_q, hq)
-            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
-            kvq_batch_attn(self.handle, layer, seq_ids, n_q, hq, causal, q.data_ptr(), softmax_scale, out.data_ptr(),
-                           0 if lse is None else lse.data_ptr(), ws.data_ptr(), nb, st)
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.batch_attn(layer, seq_ids, n_q, q, causal, out, lse, return_lse, softmax_scale)
+        n = len(seq_ids)
+        if n != len(n_q):
+            _refuse("batch_attn", "one n_q for each sequence")
+        rows, hq = self._queries("batch_attn", q, n_q)
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous() or \
+                out.get_device() != self._index:
+            _refuse("batch_attn", "out has q's shape, type and device")
+        if lse is not None:
+            self._lse("batch_attn", lse, rows, hq)
+        elif return_lse:
+            lse = q.new_empty((rows, hq), dtype=torch.float32)
+        ids, nq = _i32arr(seq_ids), _i32arr(n_q)
+        ws, ptr, nb = self._batch_workspace(layer, n, ids, nq, hq)
+        rc = _lib.kvq_batch_attn(self.handle, layer, n, ids, nq, hq, 1 if causal else 0, q.data_ptr(), softmax_scale,
+                                 out.data_ptr(), 0 if lse is None else lse.data_ptr(), ptr, nb,
+                                 self._raw_stream(self._index))
+        if rc:
+            raise KVQError(rc, "kvq_batch_attn")
         return out if lse is None else (out, lse)
-
-    def _lse(self, where, lse, q):
-        _refuse(lse.dtype != self.torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous(),
-                where, "lse is contiguous fp32 [sum(n_q), n_q_heads]")
-        self._same_device(lse, where, "lse")
-
-    def _mass_rows(self, where, x, n, name):
-        p = self.params
-        _refuse(x.dtype != self.torch.float32 or x.dim() != 3 or x.shape[0] != n or x.shape[1] != p.n_kv_heads or
-                not x.is_contiguous(), where, f"{name} is contiguous fp32 [sequences, n_kv_heads, tokens]")
-        self._same_device(x, where, name)
 
     def attn_mass(self, layer, seq_ids, n_q, q, lse, causal=False, decay=1.0, mass_in=None, mass_out=None,
                   softmax_scale=0.0, stream=None):
@@ -514,27 +561,32 @@ class KVCache:
         mass_in, mass_out: fp32 [len(seq_ids), n_kv_heads, tokens >= the longest sequence]; mass_out
         defaults to a new tensor (zeros behind each sequence); both may be one tensor."""
         torch = self.torch
-        seq_ids, n_q = list(seq_ids), list(n_q)
-        _refuse(len(seq_ids) != len(n_q), "attn_mass", "one n_q for each sequence")
-        self._queries("attn_mass", q, n_q)
-        self._lse("attn_mass", lse, q)
-        hq = q.shape[1]
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.attn_mass(layer, seq_ids, n_q, q, lse, causal, decay, mass_in, mass_out, softmax_scale)
+        n = len(seq_ids)
+        if n != len(n_q):
+            _refuse("attn_mass", "one n_q for each sequence")
+        rows, hq = self._queries("attn_mass", q, n_q)
+        self._lse("attn_mass", lse, rows, hq)
         if mass_in is None:
             decay = 0.0
         else:
-            self._mass_rows("attn_mass", mass_in, len(seq_ids), "mass_in")
-        with _Call(torch, self.storage.device, stream) as st:
-            if mass_out is None:
-                most = max([self.seq_len(layer, s) for s in seq_ids] + [1])
-                shape = (len(seq_ids), self.params.n_kv_heads, most) if mass_in is None else mass_in.shape
-                mass_out = torch.zeros(shape, dtype=torch.float32, device=self.storage.device)
-            self._mass_rows("attn_mass", mass_out, len(seq_ids), "mass_out")
-            _refuse(mass_in is not None and mass_in.shape != mass_out.shape, "attn_mass", "mass_in has mass_out's shape")
-            nb = kvq_batch_workspace_bytes(self.handle, layer, seq_ids, n_q, hq)
-            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
-            kvq_attn_mass(self.handle, layer, seq_ids, n_q, hq, causal, q.data_ptr(), softmax_scale, lse.data_ptr(),
-                          decay, 0 if mass_in is None else mass_in.data_ptr(), mass_out.data_ptr(), mass_out.shape[2],
-                          ws.data_ptr(), nb, st)
+            self._mass_rows("attn_mass", mass_in, n, "mass_in")
+        if mass_out is None:
+            most = max([self.seq_len(layer, s) for s in seq_ids] + [1])
+            shape = (n, self.params.n_kv_heads, most) if mass_in is None else mass_in.shape
+            mass_out = torch.zeros(shape, dtype=torch.float32, device=q.device)
+        ld = self._mass_rows("attn_mass", mass_out, n, "mass_out")
+        if mass_in is not None and mass_in.shape != mass_out.shape:
+            _refuse("attn_mass", "mass_in has mass_out's shape")
+        ids, nq = _i32arr(seq_ids), _i32arr(n_q)
+        ws, ptr, nb = self._batch_workspace(layer, n, ids, nq, hq)
+        rc = _lib.kvq_attn_mass(self.handle, layer, n, ids, nq, hq, 1 if causal else 0, q.data_ptr(), softmax_scale,
+                                lse.data_ptr(), decay, 0 if mass_in is None else mass_in.data_ptr(),
+                                mass_out.data_ptr(), ld, ptr, nb, self._raw_stream(self._index))
+        if rc:
+            raise KVQError(rc, "kvq_attn_mass")
         return mass_out
 
     def evict(self, dst, layer, dst_layer, seq_ids, dst_ids, mass, budget, sink=0, recent=0, kept=None, mass_out=None,
@@ -545,25 +597,36 @@ class KVCache:
         [len(seq_ids), n_kv_heads, budget], -1 behind the last; mass_out fp32 of the same shape, zeros
         behind the last)."""
         torch = self.torch
-        seq_ids, dst_ids = list(seq_ids), list(dst_ids)
-        n = len(seq_ids)
-        _refuse(len(dst_ids) != n, "evict", "one destination for each sequence")
-        self._mass_rows("evict", mass, n, "mass")
-        hkv = self.params.n_kv_heads
-        with _Call(torch, self.storage.device, stream) as st:
-            if kept is None:
-                kept = torch.empty((n, hkv, max(budget, 0)), dtype=torch.int32, device=self.storage.device)
-            if mass_out is None:
-                mass_out = torch.empty((n, hkv, max(budget, 0)), dtype=torch.float32, device=self.storage.device)
-            _refuse(kept.dtype != torch.int32 or tuple(kept.shape) != (n, hkv, budget) or not kept.is_contiguous(),
-                    "evict", "kept is contiguous int32 [sequences, n_kv_heads, budget]")
-            self._same_device(kept, "evict", "kept")
-            self._mass_rows("evict", mass_out, n, "mass_out")
-            nb = kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget)
-            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=self.storage.device)
-            kvq_evict(self.handle, layer, dst.handle, dst_layer, seq_ids, dst_ids, mass.data_ptr(), mass.shape[2],
-                      budget, sink, recent, kept.data_ptr(), mass_out.data_ptr(), mass_out.shape[2], ws.data_ptr(), nb,
-                      st)
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.evict(dst, layer, dst_layer, seq_ids, dst_ids, mass, budget, sink, recent, kept, mass_out)
+        n, hkv = len(seq_ids), self.params.n_kv_heads
+        if len(dst_ids) != n:
+            _refuse("evict", "one destination for each sequence")
+        if budget < 0:
+            _refuse("evict", "a budget below 0")
+        ld = self._mass_rows("evict", mass, n, "mass")
+        shape = (n, hkv, budget)
+        if kept is None:
+            kept = mass.new_empty(shape, dtype=torch.int32)
+        elif kept.dtype is not torch.int32 or kept.shape != shape or not kept.is_contiguous() or \
+                kept.get_device() != self._index:
+            _refuse("evict", "kept is contiguous int32 [sequences, n_kv_heads, budget] on the cache's device")
+        if mass_out is None:
+            mass_out = mass.new_empty(shape)
+            out_ld = budget
+        else:
+            out_ld = self._mass_rows("evict", mass_out, n, "mass_out")
+        rc = _lib.kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget, self._size_ref)
+        if rc:
+            raise KVQError(rc, "kvq_evict_workspace_bytes")
+        nb = max(self._size.value, 16)
+        ws = mass.new_empty(nb, dtype=torch.uint8)
+        rc = _lib.kvq_evict(self.handle, layer, dst.handle, dst_layer, n, _i32arr(seq_ids), _i32arr(dst_ids),
+                            mass.data_ptr(), ld, budget, sink, recent, kept.data_ptr(), mass_out.data_ptr(), out_ld,
+                            ws.data_ptr(), nb, self._raw_stream(self._index))
+        if rc:
+            raise KVQError(rc, "kvq_evict")
         return kept, mass_out
 
     def dequant(self, layer, seq, which, t0, t1, basis=0, out=None, stream=None):
