@@ -78,31 +78,39 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //  - a load warp fetches 128-token K and V tiles (32 KB each) with TMA into a ring of stages;
 //  - one thread issues S = Q.K^T (M = N = 128, SS) and O += P.V (P from tensor memory, V as the
 //    MN-major operand straight from the rows), S, P and O in tensor memory: 512 columns;
-//  - two softmax groups of four warps, thread = row = tensor-memory lane: group t owns query tile t
-//    (two tiles), or the key tiles j = t mod 2 (one tile: `halves`, joined in shared memory at the
-//    end).  While one group works on its scores the tensor core runs the other's products.
+//  - two softmax groups of eight warps: group t owns query tile t (two tiles), or the key tiles j = t
+//    mod 2 (one tile: `halves`, joined in shared memory at the end).  A row of a group belongs to two
+//    threads, 64 of the tile's tokens each (one thread per row left the warps waiting on their own
+//    instructions: 810 us for a causal 8k prompt of 40 heads).  While one group works on its scores
+//    the tensor core runs the other's products; a half of P is handed over as soon as it is written.
 //  - the running maximum moves only when a score passes it by 2^8 (the weights stay below 2^8, O is
-//    rescaled in tensor memory then), so most tiles need no correction.
+//    rescaled in tensor memory then), so most tiles need no correction and the two threads of a row
+//    only agree, by one barrier with an OR, that none is due.
 // Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
 constexpr int BT = 128;            // rows of a query tile, tokens of a key tile
-constexpr int NSOFT = 8;           // softmax warps
-constexpr int W_MMA = 8, W_LOAD = 9;
-constexpr int NT = 320;
+constexpr int NSOFT = 16;          // softmax warps
+constexpr int W_MMA = 16, W_LOAD = 17;
+// Five warpgroups: four of softmax, one of which the load and the MMA warp use two warps.  Launched
+// with 96 registers a thread (61440 in all): 4 x 128 x 104 + 128 x 64 = 61440.
+constexpr int NT = 640;
+constexpr int R_SOFT = 104, R_REST = 64;
 constexpr int TILE = BT * D * 2;   // bytes of a tile
 constexpr int HALF = TILE / 2;     // 64 channels of it
 constexpr int MAXST = 6;           // stages
 constexpr float TAU = 8.f;         // lazy maximum, log2 units
 constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
 constexpr int MAXSPL = 64;
+constexpr int EMU = 0x00;
 
 struct Ctl {
   uint64_t full[MAXST], empty[MAXST], tmp;
-  uint64_t s_full[2], p_full[2], o_full;
+  uint64_t s_full[2], p_full[4], o_full;  // p_full: [group][half]
   uint32_t tmem;
   int32_t abort;
+  float row[2][2][BT];  // [group][half][row]: maxima, then sums
 };
 constexpr int OFF_CTL = 7 * TILE;  // two or one query tiles and five or six stages
-constexpr int ATTN_SMEM = OFF_CTL + (int)sizeof(Ctl) + 1024;
+constexpr int ATTN_SMEM = OFF_CTL + (int)sizeof(Ctl);
 static_assert(ATTN_SMEM <= 232448, "shared memory per CTA");
 
 // The visible tokens of query token i of an entry.
@@ -110,31 +118,42 @@ __device__ __forceinline__ int64_t limit_of(const BArgs &A, const BEntry &e, int
   return A.causal ? e.n - e.nq + 1 + i : e.n;
 }
 
-// Copies query rows [row of the tile] of one tile into the swizzled layout (two 64-channel halves);
-// rows past the last are zero.  F16 products over BF16 rows convert (exact in the F16 range).
+// Copies one half (64 channels) of a query row into the swizzled layout; rows past the last are zero.
+// F16 products over BF16 rows convert (exact in the F16 range).
 template <bool F16>
-__device__ __forceinline__ void load_q_row(const BArgs &A, const uint16_t *src, uint8_t *tile, int r) {
-  uint8_t *dst = tile + (r >> 3) * 1024 + (r & 7) * 128;
+__device__ __forceinline__ void load_q_row(const BArgs &A, const uint16_t *src, uint8_t *tile, int r, int h) {
+  uint8_t *dst = tile + h * HALF + (r >> 3) * 1024 + (r & 7) * 128;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (src) v = __ldg(reinterpret_cast<const uint4 *>(src) + 8 * h + c);
-      if (F16 && !A.io_f16) v = bf16x8_to_ring(v, 1);
-      *reinterpret_cast<uint4 *>(dst + h * HALF + ((c ^ (r & 7)) << 4)) = v;
-    }
+  for (int c = 0; c < 8; ++c) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (src) v = __ldg(reinterpret_cast<const uint4 *>(src) + 8 * h + c);
+    if (F16 && !A.io_f16) v = bf16x8_to_ring(v, 1);
+    *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) = v;
   }
 }
 
+// A position in a ring of n stages: the stage and the parity of its current round.
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 template <bool F16>
 __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map, const __grid_constant__ BArgs A) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = tc::smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t *S = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t S[];
+  const uint32_t base = tc::smem_u32(S);
+  if (base & 1023u) {  // the swizzled tiles need it; no launch gives anything else
+    if (threadIdx.x == 0) atomicOr(A.status, kStatusWait);
+    return;
+  }
   Ctl &C = *reinterpret_cast<Ctl *>(S + OFF_CTL);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
   int ei = 0;
   while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
   const BEntry &e = A.e[ei];
@@ -162,10 +181,8 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       tc::mbar_init(b_full + 8 * i, 1);
       tc::mbar_init(b_empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(b_s + 8 * i, 1);
-      tc::mbar_init(b_p + 8 * i, 4);
-    }
+    for (int i = 0; i < 2; ++i) tc::mbar_init(b_s + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(b_p + 8 * i, 4);
     tc::mbar_init(b_o, 1);
     tc::mbar_init(b_tmp, 1);
     C.abort = 0;
@@ -173,144 +190,154 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   }
   if (warp == W_MMA) tc::tmem_alloc(cb + (uint32_t)offsetof(Ctl, tmem), 512);
   if (warp < NSOFT) {
-    const int t = warp >> 2, r = tid & 127;
+    const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
     if (t < ntile) {
       const int i = tok0 + t * TB + r / G;
       const bool on = r < TB * G && i < tok1;
-      load_q_row<F16>(A, on ? A.q + ((e.q0 + i) * hq + head * G + r % G) * D : nullptr, S + t * TILE, r);
+      load_q_row<F16>(A, on ? A.q + ((e.q0 + i) * hq + head * G + r % G) * D : nullptr, S + t * TILE, r, h);
     }
     tc::fence_async_smem();
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = C.tmem;
-  const int z0 = (e.slot * A.hkv + head) * A.src.sides, zv = z0 + A.src.sides - 1;
+  const uint32_t tm = __shfl_sync(FULL, C.tmem, 0);
 
-  if (warp == W_LOAD) {
-    // ---- K and V tiles in the order they are used: two tiles K0 V0 K1 V1 ..; halves K0 K1 V0 K2 V1 ..
-    int n_issued = 0;
-    auto next_stage = [&]() -> uint32_t {
-      const int st = n_issued % nst;
-      if (n_issued >= nst) tc::mbar_wait(b_empty + 8 * st, (n_issued / nst - 1) & 1, abort, A.status);
-      return (uint32_t)st;
-    };
-    auto load = [&](int j, int z, bool value) {
-      const uint32_t st = next_stage(), dst = stage0 + st * TILE;
-      const int64_t t0 = (int64_t)(j0 + j) * BT;
-      const int valid = (int)min((int64_t)BT, e.n - t0);
-      // rows past the sequence's end may hold anything: their keys are masked, their values would
-      // turn a weight of 0 into NaN, so they are zeroed before the tile is handed over
-      const bool patch = value && valid < BT;
-      const uint32_t bar = patch ? b_tmp : b_full + 8 * st;
-      if (lane == 0) {
-        tc::mbar_expect(bar, TILE);
-        tc::tma_load3(dst, &map, 0, (int)t0, z, bar);
-        tc::tma_load3(dst + HALF, &map, 64, (int)t0, z, bar);
-      }
-      if (patch) {  // (the last tile of the sequence: once per CTA)
-        tc::mbar_wait(b_tmp, 0, abort, A.status, false);
-        uint8_t *p = S + (dst - base);
-        for (int u = lane; u < (BT - valid) * 16; u += 32)
-          *reinterpret_cast<uint4 *>(p + (u & 1) * HALF + (valid + (u >> 4)) * 128 + ((u >> 1) & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        tc::fence_async_smem();
-        tc::mbar_arrive_warp(b_full + 8 * st);
-      }
-      __syncwarp();
-      ++n_issued;
-    };
-    auto keys = [&](int j) {
-      load(j, z0, false);
-      if (lo) load(j, z0 + 1, false);
-    };
-    if (nt > 0) keys(0);
-#pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
-      if (halves && j + 1 < nt) keys(j + 1);
-      load(j, zv, true);
-      if (!halves && j + 1 < nt) keys(j + 1);
-    }
-    // no copy is in flight when the CTA ends (its pipeline may have been given up)
-    for (int i = max(0, n_issued - nst); i < n_issued; ++i)
-      tc::mbar_wait(b_full + 8 * (i % nst), (i / nst) & 1, abort, A.status, false);
-  } else if (warp == W_MMA) {
-    // ---- products
-    if (lane == 0 && nt > 0) {
-      constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0), idO = tc::idesc(F16, BT, D, 1);
-      int used = 0;  // stages consumed, in load order
-      auto take = [&]() -> uint32_t {
-        const int st = used % nst;
-        tc::mbar_wait(b_full + 8 * st, (used / nst) & 1, abort, A.status);
-        ++used;
-        return (uint32_t)st;
+  if (warp >= NSOFT) {
+    tc::regs_down<R_REST>();
+    if (warp == W_LOAD) {
+      // ---- K and V tiles in the order they are used: two tiles K0 V0 K1 V1 ..; halves K0 K1 V0 K2 V1 ..
+      const int z0 = (e.slot * A.hkv + head) * A.src.sides, zv = z0 + A.src.sides - 1;
+      int n_issued = 0;
+      Ring g;
+      auto load = [&](int j, int z, bool value) {
+        if (n_issued >= nst) tc::mbar_wait(b_empty + 8 * g.at, g.phase ^ 1u, abort, A.status);
+        const uint32_t dst = stage0 + g.at * TILE, b_st = b_full + 8 * g.at;
+        const int64_t t0 = (int64_t)(j0 + j) * BT;
+        const int valid = (int)min((int64_t)BT, e.n - t0);
+        // rows past the sequence's end may hold anything: their keys are masked, their values would
+        // turn a weight of 0 into NaN, so they are zeroed before the tile is handed over
+        const bool patch = value && valid < BT;
+        const uint32_t bar = patch ? b_tmp : b_st;
+        if (lane == 0) {
+          tc::mbar_expect(bar, TILE);
+          tc::tma_load3(dst, &map, 0, (int)t0, z, bar);
+          tc::tma_load3(dst + HALF, &map, 64, (int)t0, z, bar);
+        }
+        if (patch) {  // (the last tile of the sequence: once per CTA)
+          tc::mbar_wait(b_tmp, 0, abort, A.status, false);
+          uint8_t *p = S + (dst - base);
+          for (int u = lane; u < (BT - valid) * 16; u += 32)
+            *reinterpret_cast<uint4 *>(p + (u & 1) * HALF + (valid + (u >> 4)) * 128 + ((u >> 1) & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          tc::fence_async_smem();
+          tc::mbar_arrive_warp(b_st);
+        }
+        __syncwarp();
+        ++n_issued;
+        g.next(nst);
       };
-      auto qk = [&](int t, uint32_t qtile, uint32_t st, bool first) {
-        const uint64_t q = tc::desc_sw128(qtile, 0), k = tc::desc_sw128(stage0 + st * TILE, 0);
+      auto keys = [&](int j) {
+        load(j, z0, false);
+        if (lo) load(j, z0 + 1, false);
+      };
+      if (nt > 0) keys(0);
+#pragma unroll 1
+      for (int j = 0; j < nt; ++j) {
+        if (halves && j + 1 < nt) keys(j + 1);
+        load(j, zv, true);
+        if (!halves && j + 1 < nt) keys(j + 1);
+      }
+      // no copy is in flight when the CTA ends (its pipeline may have been given up)
+      for (int i = max(0, n_issued - nst); i < n_issued; ++i)
+        tc::mbar_wait(b_full + 8 * (i % nst), (i / nst) & 1, abort, A.status, false);
+    } else if (warp == W_MMA && nt > 0) {
+      // ---- products: the whole warp waits (its values stay in uniform registers), one lane issues
+      constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0), idO = tc::idesc(F16, BT, D, 1);
+      const uint64_t dq = tc::desc_sw128(base, 0), dk = tc::desc_sw128(stage0, 0), dv = tc::desc_sw128(stage0, HALF);
+      const bool leader = tc::elect_one();
+      Ring g;
+      auto take = [&]() -> uint32_t {
+        const uint32_t st = g.at;
+        tc::mbar_wait(b_full + 8 * st, g.phase, abort, A.status);
+        g.next(nst);
+        return st;
+      };
+      auto qk = [&](int t, int qtile, uint32_t st, uint32_t acc) {
+        const uint64_t q = dq + (uint64_t)(qtile * (TILE >> 4)), k = dk + (uint64_t)(st * (TILE >> 4));
+        if (leader) {
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint64_t o = (uint64_t)((s & 3) * 2 + (s >> 2) * (HALF >> 4));  // 32 bytes along the channels
-          tc::mma_ss(tm + BT * t, q + o, k + o, idS, first && s == 0 ? 0u : 1u);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint64_t o = (uint64_t)((s & 3) * 2 + (s >> 2) * (HALF >> 4));  // 32 bytes along the channels
+            tc::mma_ss(tm + BT * t, q + o, k + o, idS, s == 0 ? acc : 1u);
+          }
         }
       };
-      auto pv = [&](int t, uint32_t st, bool first) {
-        const uint64_t v = tc::desc_sw128(stage0 + st * TILE, HALF);
+      // the j-th weights of group t, half by half as they are written: 16 tokens are 8 columns of P
+      // and two groups of 8 rows of V
+      auto pv = [&](int t, uint32_t ph, uint32_t st, uint32_t acc) {
+        const uint64_t v = dv + (uint64_t)(st * (TILE >> 4));
 #pragma unroll
-        for (int s = 0; s < BT / 16; ++s)  // 16 tokens: 8 columns of P, two groups of 8 rows of V
-          tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 8 * s, v + (uint64_t)(s * (2048 >> 4)), idO,
-                     first && s == 0 ? 0u : 1u);
+        for (int h = 0; h < 2; ++h) {
+          tc::mbar_wait(b_p + 8 * (2 * t + h), ph, abort, A.status);
+          tc::fence_after();
+          if (leader) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 8 * s, v + (uint64_t)((4 * h + s) * (2048 >> 4)), idO,
+                         h == 0 && s == 0 ? acc : 1u);
+          }
+        }
       };
-      auto wait_p = [&](int t, int j) {
-        tc::mbar_wait(b_p + 8 * t, j & 1, abort, A.status);
-        tc::fence_after();
+      auto done = [&](uint32_t bar) {
+        if (leader) tc::commit(bar);
       };
       if (!halves) {
         {
           const uint32_t k = take(), l = lo ? take() : 0;
           tc::fence_after();
+#pragma unroll
           for (int t = 0; t < 2; ++t) {
-            qk(t, base + t * TILE, k, true);
-            if (lo) qk(t, base + t * TILE, l, false);
-            tc::commit(b_s + 8 * t);
+            qk(t, t, k, 0u);
+            if (lo) qk(t, t, l, 1u);
+            done(b_s + 8 * t);
           }
-          tc::commit(b_empty + 8 * k);
-          if (lo) tc::commit(b_empty + 8 * l);
+          done(b_empty + 8 * k);
+          if (lo) done(b_empty + 8 * l);
         }
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
           const bool more = j + 1 < nt;
           const uint32_t v = take();
-          wait_p(0, j);
-          pv(0, v, j == 0);
           uint32_t k = 0, l = 0;
           if (more) {
             k = take();
             if (lo) l = take();
-            tc::fence_after();
-            qk(0, base, k, true);
-            if (lo) qk(0, base, l, false);
-            tc::commit(b_s);
           }
-          wait_p(1, j);
-          pv(1, v, j == 0);
-          tc::commit(b_empty + 8 * v);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            pv(t, j & 1, v, j > 0);
+            if (more) {
+              qk(t, t, k, 0u);
+              if (lo) qk(t, t, l, 1u);
+              done(b_s + 8 * t);
+            }
+          }
+          done(b_empty + 8 * v);
           if (more) {
-            qk(1, base + TILE, k, true);
-            if (lo) qk(1, base + TILE, l, false);
-            tc::commit(b_s + 8);
-            tc::commit(b_empty + 8 * k);
-            if (lo) tc::commit(b_empty + 8 * l);
+            done(b_empty + 8 * k);
+            if (lo) done(b_empty + 8 * l);
           }
         }
       } else {
         auto keys = [&](int j) {
           const uint32_t k = take(), l = lo ? take() : 0;
           tc::fence_after();
-          qk(j & 1, base, k, true);
-          if (lo) qk(j & 1, base, l, false);
-          tc::commit(b_s + 8 * (j & 1));
-          tc::commit(b_empty + 8 * k);
-          if (lo) tc::commit(b_empty + 8 * l);
+          qk(j & 1, 0, k, 0u);
+          if (lo) qk(j & 1, 0, l, 1u);
+          done(b_s + 8 * (j & 1));
+          done(b_empty + 8 * k);
+          if (lo) done(b_empty + 8 * l);
         };
         // S and P of a group share columns: the scores of tile j + 2 follow the product of tile j
         keys(0);
@@ -318,92 +345,115 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
           const uint32_t v = take();
-          wait_p(j & 1, j >> 1);
-          pv(j & 1, v, j < 2);
-          tc::commit(b_empty + 8 * v);
+          pv(j & 1, (j >> 1) & 1, v, j >= 2);
+          done(b_empty + 8 * v);
           if (j + 2 < nt) keys(j + 2);
         }
       }
-      tc::commit(b_o);
+      done(b_o);
       tc::mbar_wait(b_o, 0, abort, A.status, false);
     }
-    __syncwarp();
   } else {
-    // ---- softmax: thread = row of query tile t (halves: of the one tile)
-    const int t = warp >> 2, r = tid & 127;
+    tc::regs_up<R_SOFT>();
+    // ---- softmax: row r of query tile t (halves: of the one tile), tokens 64 h .. 64 h + 63 of a tile
+    const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tS = tm + lanes + BT * t, tO = tm + lanes + 2 * BT + D * t;
+    const uint32_t tS = tm + lanes + BT * t + 64 * h, tO = tm + lanes + 2 * BT + D * t + 64 * h;
+    const int pair = 1 + 4 * t + (warp & 3);  // barrier of the two warps that share these rows
     const int i = tok0 + (halves ? 0 : t * TB) + r / G;
     const bool on = r < TB * G && i < tok1;
-    const int64_t lim = on ? limit_of(A, e, i) : 0;
+    // (rows that hold no query see everything: a mask for them would hold up their warp on every tile)
+    const int64_t lim = on ? limit_of(A, e, i) : e.n;
     const int step = halves ? 2 : 1;
     float m = -INFINITY, l = 0.f;
     int u = 0;
 #pragma unroll 1
     for (int j = halves ? t : 0; j < nt; j += step, ++u) {
+      const int64_t left = lim - (int64_t)(j0 + j) * BT - 64 * h;  // visible tokens of this half tile
       tc::mbar_wait(b_s + 8 * t, u & 1, abort, A.status);
       tc::fence_after();
-      float s[BT];
+      float s[64], mx[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, s + 32 * c);
-      tc::tmem_wait_ld();
-      const int64_t left = lim - (int64_t)(j0 + j) * BT;  // visible tokens of this tile
-      if (left < BT) {
-        const int lv = (int)max((int64_t)0, left);
+      for (int v = 0; v < 8; ++v) mx[v] = -INFINITY;
+      // the first 32 are searched for their maximum while the others are read
+      tc::tmem_ld32(tS, s);
 #pragma unroll
-        for (int c = 0; c < BT; ++c)
-          if (c >= lv) s[c] = -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+      for (int c = 0; c < 2; ++c) {
+        tc::tmem_wait_ld();
+        if (c == 0) tc::tmem_ld32(tS + 32, s + 32);
+        if (left < 64) {
+          const int lv = (int)max((int64_t)0, left);
 #pragma unroll
-      for (int c = 4; c < BT; c += 4) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) mx[v] = fmaxf(mx[v], s[c + v]);
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.qscale;
-      float alpha = 1.f;
-      if (top > m + TAU) {  // also the first scores a row sees (m = -inf, alpha = 0)
-        alpha = tc::ex2(m - top);
-        m = top;
-        l *= alpha;
-      }
-      if (u > 0 && __any_sync(FULL, alpha != 1.f)) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          tc::tmem_ld32(tO + 32 * c, o);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int v = 0; v < 32; ++v) o[v] *= alpha;
-          tc::tmem_st32(tO + 32 * c, reinterpret_cast<const uint32_t *>(o));
+          for (int v = 0; v < 32; ++v)
+            if (32 * c + v >= lv) s[32 * c + v] = -INFINITY;
         }
-        tc::tmem_wait_st();
+#pragma unroll
+        for (int v = 0; v < 32; v += 16) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[32 * c + v + k]), s[32 * c + v + 8 + k]);
+        }
+      }
+      const float top =
+          fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
+          A.qscale;
+      if (tc::bar_any(pair, 64, top > m + TAU)) {
+        // a row's first scores, or some far above the maximum in use: both threads take the new one
+        C.row[t][h][r] = top;
+        tc::bar_sync(pair, 64);
+        const float both = fmaxf(top, C.row[t][h ^ 1][r]);
+        float alpha = 1.f;
+        if (both > m + TAU) {
+          alpha = tc::ex2(m - both);  // (m = -inf, nothing summed yet: 0)
+          m = both;
+          l *= alpha;
+        }
+        if (u > 0 && __any_sync(FULL, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float o[32];
+            tc::tmem_ld32(tO + 32 * c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int v = 0; v < 32; ++v) o[v] *= alpha;
+            tc::tmem_st32(tO + 32 * c, reinterpret_cast<const uint32_t *>(o));
+          }
+          tc::tmem_wait_st();
+          tc::fence_before();
+        }
+        // (a half of P lets the product add to every channel: both halves are rescaled by then)
+        tc::bar_sync(pair, 64);
+        tc::fence_after();
       }
       const float sub = m == -INFINITY ? 0.f : -m;
       const tc::f2 sc = tc::pack2(A.qscale, A.qscale), ms = tc::pack2(sub, sub);
-      tc::f2 sum[2] = {0ull, 0ull};
+      tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+      uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
-#pragma unroll
-        for (int v = 0; v < 32; ++v) {
-          float x0, x1;
-          tc::unpack2(tc::fma2(tc::pack2(s[64 * c + 2 * v], s[64 * c + 2 * v + 1]), sc, ms), x0, x1);
+      for (int v = 0; v < 32; ++v) {
+        float x0, x1;
+        const tc::f2 x = tc::fma2(tc::pack2(s[2 * v], s[2 * v + 1]), sc, ms);
+        if ((EMU >> (v & 7)) & 1) {
+          tc::ex2_fma<4>(x, x0, x1);
+        } else {
+          tc::unpack2(x, x0, x1);
           x0 = tc::ex2(x0);
           x1 = tc::ex2(x1);
-          sum[v & 1] = tc::add2(sum[v & 1], tc::pack2(x0, x1));
-          w[v] = tc::round2<F16>(x0, x1);
         }
-        tc::tmem_st32(tS + 32 * c, w);
+        sum[v & 3] = tc::add2(sum[v & 3], tc::pack2(x0, x1));
+        w[v] = tc::round2<F16>(x0, x1);
       }
-      float l0, l1;
-      tc::unpack2(tc::add2(sum[0], sum[1]), l0, l1);
-      l += l0 + l1;
+      tc::tmem_st32(tS, w);  // P over the scores this thread has read
       tc::tmem_wait_st();
       tc::fence_before();
-      tc::mbar_arrive_warp(b_p + 8 * t);
+      tc::mbar_arrive_warp(b_p + 8 * (2 * t + h));
+      float l0, l1;
+      tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), l0, l1);
+      l += l0 + l1;
     }
-    // ---- the result: this group's m, l and accumulator
+    // ---- the result: m, l of the row, 64 channels of the accumulator
+    C.row[t][h][r] = l;
+    tc::bar_sync(pair, 64);
+    l = C.row[t][0][r] + C.row[t][1][r];
     if (nt > 0) {
       tc::mbar_wait(b_o, 0, abort, A.status);
       tc::fence_after();
@@ -413,17 +463,19 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     const bool any1 = halves && nt > 1;
     if (any1 && t == 1) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         float o[32];
         tc::tmem_ld32(tO + 32 * c, o);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int v = 0; v < 32; ++v) ex[r * 129 + 32 * c + v] = o[v];
+        for (int v = 0; v < 32; ++v) ex[r * 129 + 64 * h + 32 * c + v] = o[v];
       }
-      ex[128 * 129 + 2 * r] = m;
-      ex[128 * 129 + 2 * r + 1] = l;
+      if (h == 0) {
+        ex[128 * 129 + 2 * r] = m;
+        ex[128 * 129 + 2 * r + 1] = l;
+      }
     }
-    if (any1) asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (any1) tc::bar_sync(9, 32 * NSOFT);
     if (!(halves && t == 1)) {
       float f0 = 1.f, f1 = 0.f;
       if (any1) {
@@ -439,7 +491,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       const float inv = split ? 1.f : (l > 0.f ? 1.f / l : (l == l ? 0.f : l));
       float *rec = split ? A.part + (e.part0 + ((int64_t)i * hq + head * G + r % G) * e.nsplit + sp) * PREC : nullptr;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         float o[32];
         if (nt > 0) {
           tc::tmem_ld32(tO + 32 * c, o);
@@ -448,29 +500,30 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
 #pragma unroll
           for (int v = 0; v < 32; ++v) o[v] = 0.f;
         }
+        const int ch = 64 * h + 32 * c;
         if (any1) {
 #pragma unroll
-          for (int v = 0; v < 32; ++v) o[v] = o[v] * f0 + ex[r * 129 + 32 * c + v] * f1;
+          for (int v = 0; v < 32; ++v) o[v] = o[v] * f0 + ex[r * 129 + ch + v] * f1;
         }
         if (on && split) {
 #pragma unroll
           for (int v = 0; v < 32; v += 4)
-            *reinterpret_cast<float4 *>(rec + 4 + 32 * c + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
+            *reinterpret_cast<float4 *>(rec + 4 + ch + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
         } else if (on) {
           uint32_t w[16];
 #pragma unroll
           for (int v = 0; v < 16; ++v)
             w[v] = A.io_f16 ? tc::round2<true>(o[2 * v] * inv, o[2 * v + 1] * inv)
                             : tc::round2<false>(o[2 * v] * inv, o[2 * v + 1] * inv);
-          uint4 *dst = reinterpret_cast<uint4 *>(A.out + row * D + 32 * c);
+          uint4 *dst = reinterpret_cast<uint4 *>(A.out + row * D + ch);
 #pragma unroll
           for (int v = 0; v < 4; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
         }
       }
-      if (on && split) {
+      if (on && split && h == 0) {
         rec[0] = m;
         rec[1] = l;
-      } else if (on && A.lse) {
+      } else if (on && A.lse && h == 0) {
         A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
       }
     }
@@ -551,22 +604,26 @@ constexpr int OFF_MCTL = (NKS + NQS) * TILE;
 struct MCtl {
   uint64_t k_full[NKS], k_empty[NKS], q_full[NQS], q_empty[NQS], s_full[4], s_empty[4], tmp, last;
   alignas(16) float nlse[NQS][BT];  // -lse * log2(e) of the tile's rows
+  float half[2][BT];                // sums of the second half of the columns
   uint32_t tmem;
   int32_t abort;
 };
-constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl) + 1024;
+constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl);
+constexpr int MEMU = 0x0;
 static_assert(MASS_SMEM <= 232448, "shared memory per CTA");
 
 template <bool F16>
 __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensorMap kmap,
                                                 const __grid_constant__ CUtensorMap qmap,
                                                 const __grid_constant__ BArgs A) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = tc::smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t *S = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t S[];
+  const uint32_t base = tc::smem_u32(S);
+  if (base & 1023u) {  // the swizzled tiles need it; no launch gives anything else
+    if (threadIdx.x == 0) atomicOr(A.status, kStatusWait);
+    return;
+  }
   MCtl &C = *reinterpret_cast<MCtl *>(S + OFF_MCTL);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
   int ei = 0;
   while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
   const BEntry &e = A.e[ei];
@@ -605,7 +662,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(b_sf + 8 * i, 1);
-      tc::mbar_init(b_se + 8 * i, 4);
+      tc::mbar_init(b_se + 8 * i, 8);
     }
     tc::mbar_init(b_tmp, 1);
     tc::mbar_init(b_last, 1);
@@ -623,7 +680,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = C.tmem;
+  const uint32_t tm = __shfl_sync(FULL, C.tmem, 0);
   const int z0 = (e.slot * A.hkv + head) * A.src.sides;
 
   if (warp == W_LOAD) {
@@ -731,11 +788,13 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
       tc::mbar_wait(b_last, 0, abort, A.status, false);
     }
     __syncwarp();
-  } else {
-    const int t = warp >> 2, r = tid & 127;
+  } else if (warp < NSOFT) {
+    // key r of the pair's tile t, the query columns 64 h .. 64 h + 63 of each tile
+    const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const tc::f2 sc2 = tc::pack2(A.qscale, A.qscale);
-    int qc = 0, sc = 0;
+    int sc = 0;
+    Ring g;
 #pragma unroll 1
     for (int p = p0; p < p1; ++p) {
       const int f = first_tile(p);
@@ -743,44 +802,47 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
       float total = 0.f, rest = 0.f;  // the sum over query tiles and what its additions rounded off
 #pragma unroll 1
       for (int a = f; a < qb; ++a) {
-        const int qi = resident ? a - f0 : qc++, st = qi % NQS;
-        tc::mbar_wait(b_qf + 8 * st, (qi / NQS) & 1, abort, A.status);
+        const int st = resident ? a - f0 : g.at;
+        tc::mbar_wait(b_qf + 8 * st, resident ? 0u : g.phase, abort, A.status);
+        if (!resident) g.next(NQS);
         if (tile0 < e.n) {
           const int b = 2 * t + (sc & 1);
           tc::mbar_wait(b_sf + 8 * b, (sc / 2) & 1, abort, A.status);
           ++sc;
           tc::fence_after();
-          const uint32_t tS = tm + lanes + BT * b;
+          const uint32_t tS = tm + lanes + BT * b + 64 * h;
           // columns below c0 are queries in front of the token (causal)
-          const int64_t hid = A.causal ? (key - (e.n - e.nq) - (int64_t)a * TB) * G : 0;
-          const int c0 = (int)max((int64_t)0, min((int64_t)BT, hid));
-          const bool masked = __any_sync(FULL, c0 > 0);
+          const int64_t hid = A.causal ? (key - (e.n - e.nq) - (int64_t)a * TB) * G - 64 * h : 0;
+          const int c0 = (int)max((int64_t)0, min((int64_t)64, hid));
+          float s[64];
+          tc::tmem_ld32(tS, s);
+          tc::tmem_ld32(tS + 32, s + 32);
+          tc::tmem_wait_ld();
+          tc::fence_before();
+          tc::mbar_arrive_warp(b_se + 8 * b);
+          if (__any_sync(FULL, c0 > 0)) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c < c0) s[c] = -INFINITY;
+          }
+          const float4 *nl = reinterpret_cast<const float4 *>(&C.nlse[st][64 * h]);
           tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float s[64];
-            tc::tmem_ld32(tS + 64 * h, s);
-            tc::tmem_ld32(tS + 64 * h + 32, s + 32);
-            tc::tmem_wait_ld();
-            if (h == 1) {
-              tc::fence_before();
-              tc::mbar_arrive_warp(b_se + 8 * b);
+          for (int c = 0; c < 16; ++c) {
+            const float4 n4 = nl[c];
+            const tc::f2 xa = tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y));
+            const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
+            float x0, x1, x2, x3;
+            if ((MEMU >> (c & 3)) & 1) {
+              tc::ex2_fma<5>(xa, x0, x1);
+            } else {
+              tc::unpack2(xa, x0, x1);
+              x0 = tc::ex2(x0);
+              x1 = tc::ex2(x1);
             }
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (64 * h + c < c0) s[c] = -INFINITY;
-            }
-            const float4 *nl = reinterpret_cast<const float4 *>(&C.nlse[st][64 * h]);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float4 n4 = nl[c];
-              float x0, x1, x2, x3;
-              tc::unpack2(tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y)), x0, x1);
-              tc::unpack2(tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w)), x2, x3);
-              sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(tc::ex2(x0), tc::ex2(x1)));
-              sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
-            }
+            tc::unpack2(xb, x2, x3);
+            sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(x0, x1));
+            sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
           }
           float v0, v1;
           tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), v0, v1);
@@ -790,8 +852,10 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
         }
         if (!resident) tc::mbar_arrive_warp(b_qe + 8 * st);
       }
-      if (key < e.n) {
-        const float v = total + rest;
+      if (h == 1) C.half[t][r] = total + rest;
+      tc::bar_sync(1 + 4 * t + (warp & 3), 64);
+      if (h == 0 && key < e.n) {
+        const float v = total + rest + C.half[t][r];
         if (e.mqs > 1) {
           A.part[e.mpart0 + ((int64_t)qs * A.hkv + head) * ((e.n + 3) & ~3ll) + key] = v;
         } else {
@@ -799,6 +863,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
           A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
         }
       }
+      tc::bar_sync(1 + 4 * t + (warp & 3), 64);  // (the half sum is read before the next one is written)
     }
   }
   tc::fence_before();

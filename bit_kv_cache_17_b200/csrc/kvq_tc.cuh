@@ -9,7 +9,6 @@
 namespace kvq {
 namespace tc {
 
-constexpr uint32_t kSuspendNs = 100000;       // longest suspension of one mbarrier test (100 us)
 constexpr long long kWaitCycles = 1ll << 31;  // a wait gives up after about a second
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -30,12 +29,14 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+// (no suspend-time operand: with one, a wait on a barrier that has already completed took 209 cycles
+// instead of 56, which alone halved the rate of the thread that issues the products)
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -43,9 +44,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // set, the status word marked); once the flag is set the waits that follow it return at once, so a
 // CTA whose pipeline broke still runs to its end.  follow = false: waits for copies and products in
 // flight, which need no other role, before the CTA releases what they write to.
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *status,
-                                          bool follow = true) {
-  if (mbar_try(bar, parity)) return;
+__device__ __forceinline__ void mbar_wait_long(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *status,
+                                            bool follow) {
   const long long t0 = clock64();
   for (;;) {
     if (mbar_try(bar, parity)) return;
@@ -56,6 +56,22 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatil
       return;
     }
   }
+}
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *status,
+                                          bool follow = true) {
+  if (__builtin_expect(!mbar_try(bar, parity), 0)) mbar_wait_long(bar, parity, abort, status, follow);
+}
+
+// named barrier of n threads; or_any: the OR of their predicates
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool bar_any(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -143,6 +159,13 @@ __device__ __forceinline__ void tmem_free(uint32_t t, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols));
 }
 
+// Moves registers between warpgroups (every warp of the warpgroup executes it).  The sum over the
+// warpgroups stays within what the block was launched with.
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,6 +194,52 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   f2 d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 2^x of a pair on the FMA pipe, for a share of the exponentials beside the 16 a cycle of the MUFU
+// unit: x = n + f with |f| <= 1/2 (n from adding and subtracting 1.5 * 2^23), 2^f by the polynomial of
+// degree DEG with the least largest relative error on that interval (Remez exchange: 2.6e-6 for 4,
+// 7.5e-8 for 5), n added to the exponent bits.  x below -126 gives 2^-126; x stays below 128.
+template <int DEG>
+__device__ __forceinline__ void ex2_fma(f2 x, float &y0, float &y1) {
+  float a, b;
+  unpack2(x, a, b);
+  x = pack2(max_nan(a, -126.f), max_nan(b, -126.f));
+  const f2 magic = pack2(12582912.f, 12582912.f), back = pack2(-12582912.f, -12582912.f);
+  const f2 t = add2(x, magic);
+  const f2 f = fma2(add2(t, back), pack2(-1.f, -1.f), x);
+  f2 p;
+  if constexpr (DEG == 4) {
+    p = fma2(pack2(0.009570102207362652f, 0.009570102207362652f), f, pack2(0.05591785907745361f, 0.05591785907745361f));
+    p = fma2(p, f, pack2(0.240247443318367f, 0.240247443318367f));
+    p = fma2(p, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+    p = fma2(p, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  } else {
+    p = fma2(pack2(0.0013276472454890609f, 0.0013276472454890609f), f, pack2(0.009675540961325169f, 0.009675540961325169f));
+    p = fma2(p, f, pack2(0.05550713092088699f, 0.05550713092088699f));
+    p = fma2(p, f, pack2(0.24022120237350464f, 0.24022120237350464f));
+    p = fma2(p, f, pack2(0.6931469440460205f, 0.6931469440460205f));
+    p = fma2(p, f, pack2(1.0000001192092896f, 1.0000001192092896f));
+  }
+  float p0, p1, t0, t1;
+  unpack2(p, p0, p1);
+  unpack2(t, t0, t1);
+  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // two fp32 rounded to a pair of F16 or BF16 (element 0 low)
