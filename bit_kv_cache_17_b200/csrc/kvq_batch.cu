@@ -100,10 +100,10 @@ constexpr int MAXST = 6;           // stages
 constexpr float TAU = 8.f;         // lazy maximum, log2 units
 constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
 constexpr int MAXSPL = 64;
-constexpr int EMU = 0x00;
+constexpr int EMU = 0x10;
 
 struct Ctl {
-  uint64_t full[MAXST], empty[MAXST], tmp;
+  uint64_t full[MAXST], empty[MAXST], tmp, q_full;
   uint64_t s_full[2], p_full[4], o_full;  // p_full: [group][half]
   uint32_t tmem;
   int32_t abort;
@@ -116,20 +116,6 @@ static_assert(ATTN_SMEM <= 232448, "shared memory per CTA");
 // The visible tokens of query token i of an entry.
 __device__ __forceinline__ int64_t limit_of(const BArgs &A, const BEntry &e, int i) {
   return A.causal ? e.n - e.nq + 1 + i : e.n;
-}
-
-// Copies one half (64 channels) of a query row into the swizzled layout; rows past the last are zero.
-// F16 products over BF16 rows convert (exact in the F16 range).
-template <bool F16>
-__device__ __forceinline__ void load_q_row(const BArgs &A, const uint16_t *src, uint8_t *tile, int r, int h) {
-  uint8_t *dst = tile + h * HALF + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (src) v = __ldg(reinterpret_cast<const uint4 *>(src) + 8 * h + c);
-    if (F16 && !A.io_f16) v = bf16x8_to_ring(v, 1);
-    *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) = v;
-  }
 }
 
 // A position in a ring of n stages: the stage and the parity of its current round.
@@ -145,7 +131,9 @@ struct Ring {
 };
 
 template <bool F16>
-__global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map, const __grid_constant__ BArgs A) {
+__global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
+                                                const __grid_constant__ CUtensorMap qmap,
+                                                const __grid_constant__ BArgs A) {
   extern __shared__ __align__(1024) uint8_t S[];
   const uint32_t base = tc::smem_u32(S);
   if (base & 1023u) {  // the swizzled tiles need it; no launch gives anything else
@@ -174,7 +162,9 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   const uint32_t b_full = cb + (uint32_t)offsetof(Ctl, full), b_empty = cb + (uint32_t)offsetof(Ctl, empty);
   const uint32_t b_s = cb + (uint32_t)offsetof(Ctl, s_full), b_p = cb + (uint32_t)offsetof(Ctl, p_full);
   const uint32_t b_o = cb + (uint32_t)offsetof(Ctl, o_full), b_tmp = cb + (uint32_t)offsetof(Ctl, tmp);
+  const uint32_t b_q = cb + (uint32_t)offsetof(Ctl, q_full);
   volatile int32_t *abort = &C.abort;
+  const int z0 = (e.slot * A.hkv + head) * A.src.sides, zv = z0 + A.src.sides - 1;
 
   if (warp == W_LOAD && lane == 0) {
     for (int i = 0; i < MAXST; ++i) {
@@ -185,19 +175,30 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     for (int i = 0; i < 4; ++i) tc::mbar_init(b_p + 8 * i, 4);
     tc::mbar_init(b_o, 1);
     tc::mbar_init(b_tmp, 1);
+    tc::mbar_init(b_q, 1);
     C.abort = 0;
     tc::fence_mbar_init();
+    // the query tiles and the first keys are on their way while the rest is set up.  A tile takes
+    // whatever rows follow an entry's last one too: rows do not mix, and those are never written out
+    const uint32_t bytes = 2 * TB * G * 128;
+    tc::mbar_expect(b_q, ntile * bytes);
+    for (int t = 0; t < ntile; ++t)
+      for (int h = 0; h < 2; ++h)
+        tc::tma_load4(base + t * TILE + h * HALF, &qmap, 64 * h, 0, head, (int)(e.q0 + tok0 + t * TB), b_q);
+    if (nt > 0) {
+      tc::mbar_expect(b_full, TILE);
+      tc::tma_load3(stage0, &map, 0, j0 * BT, z0, b_full);
+      tc::tma_load3(stage0 + HALF, &map, 64, j0 * BT, z0, b_full);
+    }
   }
   if (warp == W_MMA) tc::tmem_alloc(cb + (uint32_t)offsetof(Ctl, tmem), 512);
-  if (warp < NSOFT) {
-    const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
-    if (t < ntile) {
-      const int i = tok0 + t * TB + r / G;
-      const bool on = r < TB * G && i < tok1;
-      load_q_row<F16>(A, on ? A.q + ((e.q0 + i) * hq + head * G + r % G) * D : nullptr, S + t * TILE, r, h);
-    }
-    tc::fence_async_smem();
+  // rows of a tile that no copy writes
+  for (int u = tid; u < ntile * (BT - TB * G) * 16; u += NT) {
+    const int t = u / ((BT - TB * G) * 16), v = u % ((BT - TB * G) * 16);
+    *reinterpret_cast<uint4 *>(S + t * TILE + (v & 1) * HALF + (TB * G + (v >> 4)) * 128 + ((v >> 1) & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
   }
+  tc::fence_async_smem();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -207,7 +208,6 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     tc::regs_down<R_REST>();
     if (warp == W_LOAD) {
       // ---- K and V tiles in the order they are used: two tiles K0 V0 K1 V1 ..; halves K0 K1 V0 K2 V1 ..
-      const int z0 = (e.slot * A.hkv + head) * A.src.sides, zv = z0 + A.src.sides - 1;
       int n_issued = 0;
       Ring g;
       auto load = [&](int j, int z, bool value) {
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         // turn a weight of 0 into NaN, so they are zeroed before the tile is handed over
         const bool patch = value && valid < BT;
         const uint32_t bar = patch ? b_tmp : b_st;
-        if (lane == 0) {
+        if (lane == 0 && n_issued > 0) {  // (the first tile has been asked for above)
           tc::mbar_expect(bar, TILE);
           tc::tma_load3(dst, &map, 0, (int)t0, z, bar);
           tc::tma_load3(dst + HALF, &map, 64, (int)t0, z, bar);
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       // no copy is in flight when the CTA ends (its pipeline may have been given up)
       for (int i = max(0, n_issued - nst); i < n_issued; ++i)
         tc::mbar_wait(b_full + 8 * (i % nst), (i / nst) & 1, abort, A.status, false);
+      tc::mbar_wait(b_q, 0, abort, A.status, false);
     } else if (warp == W_MMA && nt > 0) {
       // ---- products: the whole warp waits (its values stay in uniform registers), one lane issues
       constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0), idO = tc::idesc(F16, BT, D, 1);
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       auto done = [&](uint32_t bar) {
         if (leader) tc::commit(bar);
       };
+      tc::mbar_wait(b_q, 0, abort, A.status);
       if (!halves) {
         {
           const uint32_t k = take(), l = lo ? take() : 0;
@@ -509,15 +511,30 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
 #pragma unroll
           for (int v = 0; v < 32; v += 4)
             *reinterpret_cast<float4 *>(rec + 4 + ch + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
-        } else if (on) {
-          uint32_t w[16];
+        } else if (!split) {
+          // through the query tile (no product reads it any more), in its layout
+          uint8_t *dst = S + t * TILE + h * HALF + r * 128;
 #pragma unroll
-          for (int v = 0; v < 16; ++v)
-            w[v] = A.io_f16 ? tc::round2<true>(o[2 * v] * inv, o[2 * v + 1] * inv)
-                            : tc::round2<false>(o[2 * v] * inv, o[2 * v + 1] * inv);
-          uint4 *dst = reinterpret_cast<uint4 *>(A.out + row * D + ch);
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+            for (int k = 0; k < 4; ++k)
+              w[k] = A.io_f16 ? tc::round2<true>(o[8 * v + 2 * k] * inv, o[8 * v + 2 * k + 1] * inv)
+                              : tc::round2<false>(o[8 * v + 2 * k] * inv, o[8 * v + 2 * k + 1] * inv);
+            *reinterpret_cast<uint4 *>(dst + (((4 * c + v) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (!split) {
+        // whole rows to memory, two per warp and instruction
+        tc::bar_sync(10 + t, 256);
+        const uint8_t *src = S + t * TILE;
+        const int rows = min(TB, tok1 - tok0 - (halves ? 0 : t * TB)) * G;  // (below 0: none)
+        for (int p = tid & 255; p < rows * 16; p += 256) {
+          const int rr = p >> 4, c = p & 15;
+          const int64_t at = (e.q0 + tok0 + (halves ? 0 : t * TB) + rr / G) * hq + head * G + rr % G;
+          *reinterpret_cast<uint4 *>(A.out + at * D + 8 * c) =
+              *reinterpret_cast<const uint4 *>(src + (c >> 3) * HALF + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
         }
       }
       if (on && split && h == 0) {
@@ -1178,6 +1195,20 @@ int map_queries(const void *q, int f16, int hkv, int G, int64_t rows, CUtensorMa
              : KVQ_E_CUDA;
 }
 
+// The query rows as the kernels read them: converted first where a BF16 tail meets F16 products.
+int make_queries(const Plan &P, const void *q, int f16, int hkv, int n_q_heads, void *workspace, cudaStream_t st,
+                 CUtensorMap *map) {
+  if (P.q16_bytes) {
+    uint4 *q16 = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(workspace) + P.rebuilt_bytes + P.part_bytes);
+    const int64_t n = P.rows * n_q_heads * (D / 8);
+    k_q16<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(static_cast<const uint4 *>(q), q16, n);
+    if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
+    note_launches(1);
+    q = q16;
+  }
+  return map_queries(q, f16, hkv, n_q_heads / hkv, P.rows, map);
+}
+
 // The dynamic shared memory of a kernel, allowed once per device.
 template <typename K>
 bool allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done) {
@@ -1193,10 +1224,10 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done) {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <bool F16>
-int run_attn(const CUtensorMap &map, const BArgs &A, unsigned ctas, cudaStream_t st) {
+int run_attn(const CUtensorMap &map, const CUtensorMap &qmap, const BArgs &A, unsigned ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(k_attn<F16>, ATTN_SMEM, done)) return KVQ_E_CUDA;
-  k_attn<F16><<<ctas, NT, ATTN_SMEM, st>>>(map, A);
+  k_attn<F16><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
   if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
   note_launches(1);
   return KVQ_OK;
@@ -1240,8 +1271,9 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BArgs A{};
   if (const int rc = make_source(c, layer, P, true, workspace, st, &A.src)) return rc;
-  CUtensorMap map;
+  CUtensorMap map, qmap;
   if (const int rc = map_rows(A.src, c->p.n_kv_heads, &map)) return rc;
+  if (const int rc = make_queries(P, q, A.src.f16, c->p.n_kv_heads, n_q_heads, workspace, st, &qmap)) return rc;
   A.hkv = c->p.n_kv_heads;
   A.G = n_q_heads / c->p.n_kv_heads;
   A.causal = causal;
@@ -1266,7 +1298,8 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
     }
     if (ctas == 0) continue;
     if (ctas > INT32_MAX) return KVQ_E_UNSUPPORTED;
-    if (const int rc = A.src.f16 ? run_attn<true>(map, A, (unsigned)ctas, st) : run_attn<false>(map, A, (unsigned)ctas, st))
+    if (const int rc = A.src.f16 ? run_attn<true>(map, qmap, A, (unsigned)ctas, st)
+                                 : run_attn<false>(map, qmap, A, (unsigned)ctas, st))
       return rc;
     if (joins == 0) continue;
     k_attn_join<<<(unsigned)((joins + 7) / 8), 256, 0, st>>>(A, joins);
@@ -1310,22 +1343,12 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   A.mass_out = mass_out;
   A.mass_ld = mass_ld;
   A.decay = decay;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  A.part = reinterpret_cast<float *>(ws + P.rebuilt_bytes);
+  A.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + P.rebuilt_bytes);
   A.status = reinterpret_cast<int32_t *>(c->base + c->off_status);
   CUtensorMap kmap, qmap{};
   if (const int rc = map_rows(A.src, A.hkv, &kmap)) return rc;
-  if (P.rows > 0) {
-    if (P.q16_bytes) {
-      uint4 *q16 = reinterpret_cast<uint4 *>(ws + P.rebuilt_bytes + P.part_bytes);
-      const int64_t n = P.rows * n_q_heads * (D / 8);
-      k_q16<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(static_cast<const uint4 *>(q), q16, n);
-      if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
-      note_launches(1);
-      q = q16;
-    }
-    if (const int rc = map_queries(q, A.src.f16, A.hkv, A.G, P.rows, &qmap)) return rc;
-  }
+  if (P.rows > 0)
+    if (const int rc = make_queries(P, q, A.src.f16, A.hkv, n_q_heads, workspace, st, &qmap)) return rc;
   for (size_t base = 0; base < P.e.size(); base += MAXE) {
     const int ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
     int64_t ctas = 0, joins = 0;
