@@ -36,6 +36,7 @@ struct BEntry {
   int32_t mgroup;   // weights: groups of key pairs per KV head,
   int32_t mpairs;   // pairs of key tiles in each,
   int32_t mqs, mqc; // splits of the query tiles, tiles in each
+  int32_t mtb;      // query tokens per tile (as even as the number of tiles allows)
   int64_t mpart0;   // first partial sum (mqs > 1): [split][head][n rounded up to 4]
 };
 
@@ -613,8 +614,8 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ BArgs
 // a pair belong to the two groups of four warps and share each query tile.  Up to three query tiles
 // stay in shared memory while the keys stream past (a window of queries: each key is read once, HBM
 // bound); more of them stream for each pair (a prompt: bound by the exponentials, 16 a cycle and SM).
-// Query tiles come by TMA as [token][head] rows of 64 channels; rows that belong to no query of the
-// entry are zeroed and their lse is +inf, so they add exactly 0.
+// Query tiles come by TMA as [token][head] rows of 64 channels, the tokens spread evenly over the
+// tiles; only the columns that hold queries are exponentiated, in steps of 8.
 constexpr int NKS = 4, NQS = 3;  // key and query stages
 constexpr int OFF_MCTL = (NKS + NQS) * TILE;
 
@@ -644,13 +645,13 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   int ei = 0;
   while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
   const BEntry &e = A.e[ei];
-  const int G = A.G, hq = A.hkv * G, TB = BT / G;
+  const int G = A.G, hq = A.hkv * G, TB = e.mtb, box = BT / G;  // tokens of a tile, of a copy
   const int local = blockIdx.x - e.cta0;
   const int qs = local % e.mqs, head = local / e.mqs % A.hkv;
   const int grp = local / e.mqs / A.hkv;  // the first keys (causal: seen by most queries) first
   const int npair = (int)((e.n + 2 * BT - 1) / (2 * BT));
   const int p0 = grp * e.mpairs, p1 = min(npair, p0 + e.mpairs);
-  const int nqt = (e.nq + TB - 1) / TB;
+  const int nqt = (e.nq + TB - 1) / TB;  // tiles of query tokens
   const int qb = min(nqt, (qs + 1) * e.mqc);
   // first query tile of this split that sees any key of pair p
   auto first_tile = [&](int p) -> int {
@@ -687,13 +688,6 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
     tc::fence_mbar_init();
   }
   if (warp == W_MMA) tc::tmem_alloc(cb + (uint32_t)offsetof(MCtl, tmem), 512);
-  // rows of the query stages that no copy writes
-  for (int u = tid; u < NQS * (BT - TB * G) * 16; u += NT) {
-    const int st = u / ((BT - TB * G) * 16), v = u % ((BT - TB * G) * 16);
-    *reinterpret_cast<uint4 *>(S + (NKS + st) * TILE + (v & 1) * HALF + (TB * G + (v >> 4)) * 128 + ((v >> 1) & 7) * 16) =
-        make_uint4(0u, 0u, 0u, 0u);
-  }
-  tc::fence_async_smem();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -701,7 +695,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   const int z0 = (e.slot * A.hkv + head) * A.src.sides;
 
   if (warp == W_LOAD) {
-    int kc = 0, qc = 0, patched = 0;
+    int kc = 0, qc = 0;
     auto load_k = [&](int64_t t0, int z) {
       const int st = kc % NKS;
       if (kc >= NKS) tc::mbar_wait(b_ke + 8 * st, (kc / NKS - 1) & 1, abort, A.status);
@@ -713,35 +707,32 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
       __syncwarp();
       ++kc;
     };
-    auto load_q = [&](int a) {
+    // the lse of a tile's columns, four per lane, fetched a tile ahead of their use
+    int off[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) off[k] = (lane + 32 * k) / G * hq + (lane + 32 * k) % G;
+    auto fetch = [&](int a, float (&v)[4]) {
+      const int nc = a < qb ? min(TB, e.nq - a * TB) * G : 0;
+      const float *src = A.lse + (e.q0 + (int64_t)a * TB) * hq + head * G;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < nc ? __ldg(src + off[k]) : -INFINITY;
+    };
+    float ahead[4];
+    auto load_q = [&](int a, bool first) {
       const int st = qc % NQS;
+      if (first) fetch(a, ahead);
       if (qc >= NQS) tc::mbar_wait(b_qe + 8 * st, (qc / NQS - 1) & 1, abort, A.status);
-      const int nc = min(TB, e.nq - a * TB) * G;
-      const bool patch = nc < TB * G;  // other entries' rows, or none, behind this entry's last
-      const uint32_t bar = patch ? b_tmp : b_qf + 8 * st, dst = q0s + st * TILE;
+      // the copy also brings the rows behind the tile's last: their columns are never added up
       if (lane == 0) {
-        tc::mbar_expect(bar, 2 * TB * G * 128);
-        tc::tma_load4(dst, &qmap, 0, 0, head, (int)(e.q0 + a * TB), bar);
-        tc::tma_load4(dst + HALF, &qmap, 64, 0, head, (int)(e.q0 + a * TB), bar);
+        tc::mbar_expect(b_qf + 8 * st, 2 * box * G * 128);
+        tc::tma_load4(q0s + st * TILE, &qmap, 0, 0, head, (int)(e.q0 + a * TB), b_qf + 8 * st);
+        tc::tma_load4(q0s + st * TILE + HALF, &qmap, 64, 0, head, (int)(e.q0 + a * TB), b_qf + 8 * st);
       }
-      for (int c = lane; c < BT; c += 32) {
-        float v = -INFINITY;
-        if (c < nc) {
-          v = __ldg(A.lse + (e.q0 + a * TB + c / G) * hq + head * G + c % G);
-          v = v == -INFINITY ? v : -v * LOG2E;
-        }
-        C.nlse[st][c] = v;
-      }
-      if (patch) {
-        tc::mbar_wait(b_tmp, patched & 1, abort, A.status, false);
-        ++patched;
-        for (int u = lane; u < (TB * G - nc) * 16; u += 32)
-          *reinterpret_cast<uint4 *>(S + (NKS + st) * TILE + (u & 1) * HALF + (nc + (u >> 4)) * 128 + ((u >> 1) & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        tc::fence_async_smem();
-        tc::mbar_arrive_warp(b_qf + 8 * st);
-      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        C.nlse[st][lane + 32 * k] = ahead[k] == -INFINITY ? -INFINITY : -ahead[k] * LOG2E;
       tc::mbar_arrive_warp(b_qf + 8 * st);
+      fetch(a + 1, ahead);
       ++qc;
     };
 #pragma unroll 1
@@ -754,57 +745,68 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
         if (lo) load_k(key0 + t * BT, z0 + 1);
       }
       if (!resident || p == p0)
-        for (int a = f; a < qb; ++a) load_q(a);
+        for (int a = f; a < qb; ++a) load_q(a, a == f);
     }
     for (int i = max(0, kc - NKS); i < kc; ++i)
       tc::mbar_wait(b_kf + 8 * (i % NKS), (i / NKS) & 1, abort, A.status, false);
     for (int i = max(0, qc - NQS); i < qc; ++i)
       tc::mbar_wait(b_qf + 8 * (i % NQS), (i / NQS) & 1, abort, A.status, false);
   } else if (warp == W_MMA) {
-    if (lane == 0) {
-      constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0);
-      int kc = 0, qc = 0, sc[2] = {0, 0};
+    constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0);
+    const uint64_t dk = tc::desc_sw128(base, 0), dq = tc::desc_sw128(q0s, 0);
+    const bool leader = tc::elect_one();
+    Ring gk, gq;
+    uint32_t used[2] = {0, 0};  // score buffers filled, per key tile of the pair
 #pragma unroll 1
-      for (int p = p0; p < p1; ++p) {
-        const int f = first_tile(p);
-        if (f >= qb) break;
-        const int nk = (int64_t)p * 2 * BT + BT < e.n ? 2 : 1, per = lo ? 2 : 1;
-        for (int u = 0; u < nk * per; ++u)
-          tc::mbar_wait(b_kf + 8 * ((kc + u) % NKS), ((kc + u) / NKS) & 1, abort, A.status);
-#pragma unroll 1
-        for (int a = f; a < qb; ++a) {
-          const int qi = resident ? a - f0 : qc++, st = qi % NQS;
-          tc::mbar_wait(b_qf + 8 * st, (qi / NQS) & 1, abort, A.status);
-          tc::fence_after();
-          const uint64_t q = tc::desc_sw128(q0s + st * TILE, 0);
+    for (int p = p0; p < p1; ++p) {
+      const int f = first_tile(p);
+      if (f >= qb) break;
+      const int nk = (int64_t)p * 2 * BT + BT < e.n ? 2 : 1;
+      uint32_t ks[4];  // the pair's stages
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t >= nk) break;
-            const int b = 2 * t + (sc[t] & 1);
-            if (sc[t] >= 2) {
-              tc::mbar_wait(b_se + 8 * b, (sc[t] / 2 - 1) & 1, abort, A.status);
-              tc::fence_after();
-            }
-            for (int h = 0; h < per; ++h) {
-              const uint64_t k = tc::desc_sw128(base + ((kc + t * per + h) % NKS) * TILE, 0);
-#pragma unroll
-              for (int s = 0; s < D / 16; ++s) {
-                const uint64_t o = (uint64_t)((s & 3) * 2 + (s >> 2) * (HALF >> 4));
-                tc::mma_ss(tm + BT * b, k + o, q + o, idS, h == 0 && s == 0 ? 0u : 1u);
-              }
-            }
-            tc::commit(b_sf + 8 * b);
-            ++sc[t];
-          }
-          if (!resident) tc::commit(b_qe + 8 * st);
-        }
-        for (int u = 0; u < nk * per; ++u) tc::commit(b_ke + 8 * ((kc + u) % NKS));
-        kc += nk * per;
+      for (int u = 0; u < 4; ++u) {
+        if (u >= nk * (lo ? 2 : 1)) break;
+        ks[u] = gk.at;
+        tc::mbar_wait(b_kf + 8 * gk.at, gk.phase, abort, A.status);
+        gk.next(NKS);
       }
-      tc::commit(b_last);
-      tc::mbar_wait(b_last, 0, abort, A.status, false);
+#pragma unroll 1
+      for (int a = f; a < qb; ++a) {
+        const uint32_t st = resident ? a - f0 : gq.at;
+        tc::mbar_wait(b_qf + 8 * st, resident ? 0u : gq.phase, abort, A.status);
+        if (!resident) gq.next(NQS);
+        const uint64_t q = dq + (uint64_t)(st * (TILE >> 4));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= nk) break;
+          const uint32_t b = 2 * t + (used[t] & 1);
+          if (used[t] >= 2) tc::mbar_wait(b_se + 8 * b, (used[t] / 2 - 1) & 1, abort, A.status);
+          ++used[t];
+          tc::fence_after();
+          auto product = [&](uint32_t kst, uint32_t acc) {
+            const uint64_t k = dk + (uint64_t)(kst * (TILE >> 4));
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint64_t o = (uint64_t)((s & 3) * 2 + (s >> 2) * (HALF >> 4));
+              tc::mma_ss(tm + BT * b, k + o, q + o, idS, s == 0 ? acc : 1u);
+            }
+          };
+          if (leader) {
+            product(lo ? ks[2 * t] : ks[t], 0u);
+            if (lo) product(ks[2 * t + 1], 1u);
+            tc::commit(b_sf + 8 * b);
+          }
+        }
+        if (!resident && leader) tc::commit(b_qe + 8 * st);
+      }
+      if (leader) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u < nk * (lo ? 2 : 1)) tc::commit(b_ke + 8 * ks[u]);
+      }
     }
-    __syncwarp();
+    if (leader) tc::commit(b_last);
+    tc::mbar_wait(b_last, 0, abort, A.status, false);
   } else if (warp < NSOFT) {
     // key r of the pair's tile t, the query columns 64 h .. 64 h + 63 of each tile
     const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
@@ -827,40 +829,52 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
           tc::mbar_wait(b_sf + 8 * b, (sc / 2) & 1, abort, A.status);
           ++sc;
           tc::fence_after();
-          const uint32_t tS = tm + lanes + BT * b + 64 * h;
-          // columns below c0 are queries in front of the token (causal)
-          const int64_t hid = A.causal ? (key - (e.n - e.nq) - (int64_t)a * TB) * G - 64 * h : 0;
+          // the tile's columns in two halves of a multiple of 8; this thread's are [0, ncol) of its half,
+          // those below c0 are queries in front of the token (causal)
+          const int nc = min(TB, e.nq - a * TB) * G, hc = (nc + 15) / 16 * 8;
+          const int ncol = h ? nc - hc : hc;
+          const uint32_t tS = tm + lanes + BT * b + h * hc;
+          const int64_t hid = A.causal ? (key - (e.n - e.nq) - (int64_t)a * TB) * G - h * hc : 0;
           const int c0 = (int)max((int64_t)0, min((int64_t)64, hid));
+          const bool masked = __any_sync(FULL, c0 > 0);
+          const float4 *nl = reinterpret_cast<const float4 *>(&C.nlse[st][h * hc]);
+          tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
           float s[64];
+          auto eight = [&](int k) {  // columns 8 k .. 8 k + 7
+            if (8 * k >= ncol) return;
+            if (masked || 8 * k + 8 > ncol) {
+#pragma unroll
+              for (int c = 8 * k; c < 8 * k + 8; ++c)
+                if (c < c0 || c >= ncol) s[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 2 * k; c < 2 * k + 2; ++c) {
+              const float4 n4 = nl[c];
+              const tc::f2 xa = tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y));
+              const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
+              float x0, x1, x2, x3;
+              if ((MEMU >> (c & 3)) & 1) {
+                tc::ex2_fma<5>(xa, x0, x1);
+              } else {
+                tc::unpack2(xa, x0, x1);
+                x0 = tc::ex2(x0);
+                x1 = tc::ex2(x1);
+              }
+              tc::unpack2(xb, x2, x3);
+              sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(x0, x1));
+              sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
+            }
+          };
           tc::tmem_ld32(tS, s);
-          tc::tmem_ld32(tS + 32, s + 32);
           tc::tmem_wait_ld();
+          if (ncol > 32) tc::tmem_ld32(tS + 32, s + 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) eight(k);
+          if (ncol > 32) tc::tmem_wait_ld();
           tc::fence_before();
           tc::mbar_arrive_warp(b_se + 8 * b);
-          if (__any_sync(FULL, c0 > 0)) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c < c0) s[c] = -INFINITY;
-          }
-          const float4 *nl = reinterpret_cast<const float4 *>(&C.nlse[st][64 * h]);
-          tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float4 n4 = nl[c];
-            const tc::f2 xa = tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y));
-            const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
-            float x0, x1, x2, x3;
-            if ((MEMU >> (c & 3)) & 1) {
-              tc::ex2_fma<5>(xa, x0, x1);
-            } else {
-              tc::unpack2(xa, x0, x1);
-              x0 = tc::ex2(x0);
-              x1 = tc::ex2(x1);
-            }
-            tc::unpack2(xb, x2, x3);
-            sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(x0, x1));
-            sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
-          }
+          for (int k = 4; k < 8; ++k) eight(k);
           float v0, v1;
           tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), v0, v1);
           const float v = v0 + v1, n = total + v, d = n - total;
@@ -1063,6 +1077,7 @@ void plan_mass(BEntry *e, int ne, int hkv, int G, int sms, int64_t *floats) {
   }
   for (int i = 0; i < ne; ++i) {
     const int64_t np = (e[i].n + 2 * BT - 1) / (2 * BT), qt = std::max<int64_t>(1, ((int64_t)e[i].nq + TB - 1) / TB);
+    e[i].mtb = (int)std::max<int64_t>(1, (e[i].nq + qt - 1) / qt);
     e[i].mqs = heavy ? (int)((qt + target - 1) / target) : 1;
     e[i].mqc = (int)((qt + e[i].mqs - 1) / e[i].mqs);
     e[i].mpairs = (int)(heavy ? std::max<int64_t>(1, std::min(np, target / qt)) : lo);
