@@ -627,7 +627,7 @@ struct MCtl {
   int32_t abort;
 };
 constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl);
-constexpr int MEMU = 0x0;
+constexpr int MEMU = 0x1;
 static_assert(MASS_SMEM <= 232448, "shared memory per CTA");
 
 template <bool F16>
@@ -812,80 +812,93 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
     const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const tc::f2 sc2 = tc::pack2(A.qscale, A.qscale);
-    int sc = 0;
+    const int n = (int)e.n, nq = e.nq, past = n - nq;  // (fewer than 2^31 tokens)
+    const bool causal = A.causal;
+    uint32_t sc = 0;
     Ring g;
 #pragma unroll 1
     for (int p = p0; p < p1; ++p) {
       const int f = first_tile(p);
-      const int64_t tile0 = (int64_t)p * 2 * BT + t * BT, key = tile0 + r;
+      const int tile0 = p * 2 * BT + t * BT, key = tile0 + r;
       float total = 0.f, rest = 0.f;  // the sum over query tiles and what its additions rounded off
 #pragma unroll 1
       for (int a = f; a < qb; ++a) {
         const int st = resident ? a - f0 : g.at;
         tc::mbar_wait(b_qf + 8 * st, resident ? 0u : g.phase, abort, A.status);
         if (!resident) g.next(NQS);
-        if (tile0 < e.n) {
-          const int b = 2 * t + (sc & 1);
-          tc::mbar_wait(b_sf + 8 * b, (sc / 2) & 1, abort, A.status);
-          ++sc;
-          tc::fence_after();
+        if (tile0 < n) {
           // the tile's columns in two halves of a multiple of 8; this thread's are [0, ncol) of its half,
           // those below c0 are queries in front of the token (causal)
-          const int nc = min(TB, e.nq - a * TB) * G, hc = (nc + 15) / 16 * 8;
+          const int tok = a * TB, nc = min(TB, nq - tok) * G, hc = (nc + 15) / 16 * 8;
           const int ncol = h ? nc - hc : hc;
-          const uint32_t tS = tm + lanes + BT * b + h * hc;
-          const int64_t hid = A.causal ? (key - (e.n - e.nq) - (int64_t)a * TB) * G - h * hc : 0;
-          const int c0 = (int)max((int64_t)0, min((int64_t)64, hid));
-          const bool masked = __any_sync(FULL, c0 > 0);
+          const bool diag = causal && tile0 + BT - 1 - past > tok;
+          const int c0 = diag ? min(max(key - past - tok, 0), BT) * G - h * hc : 0;
+          const uint32_t b = 2 * t + (sc & 1), tS = tm + lanes + BT * b + h * hc;
           const float4 *nl = reinterpret_cast<const float4 *>(&C.nlse[st][h * hc]);
+          tc::mbar_wait(b_sf + 8 * b, (sc >> 1) & 1, abort, A.status);
+          ++sc;
+          tc::fence_after();
           tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
           float s[64];
-          auto eight = [&](int k) {  // columns 8 k .. 8 k + 7
-            if (8 * k >= ncol) return;
-            if (masked || 8 * k + 8 > ncol) {
+          auto mask = [&](int from, int to) {
 #pragma unroll
-              for (int c = 8 * k; c < 8 * k + 8; ++c)
-                if (c < c0 || c >= ncol) s[c] = -INFINITY;
+            for (int c = 0; c < 64; ++c)
+              if (c >= from && c < to && (c < c0 || c >= ncol)) s[c] = -INFINITY;
+          };
+          auto four = [&](int c) {  // columns 4 c .. 4 c + 3
+            const float4 n4 = nl[c];
+            const tc::f2 xa = tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y));
+            const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
+            float x0, x1, x2, x3;
+            if ((MEMU >> (c & 3)) & 1) {
+              tc::ex2_fma<5>(xa, x0, x1);
+            } else {
+              tc::unpack2(xa, x0, x1);
+              x0 = tc::ex2(x0);
+              x1 = tc::ex2(x1);
             }
-#pragma unroll
-            for (int c = 2 * k; c < 2 * k + 2; ++c) {
-              const float4 n4 = nl[c];
-              const tc::f2 xa = tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y));
-              const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
-              float x0, x1, x2, x3;
-              if ((MEMU >> (c & 3)) & 1) {
-                tc::ex2_fma<5>(xa, x0, x1);
-              } else {
-                tc::unpack2(xa, x0, x1);
-                x0 = tc::ex2(x0);
-                x1 = tc::ex2(x1);
-              }
-              tc::unpack2(xb, x2, x3);
-              sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(x0, x1));
-              sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
-            }
+            tc::unpack2(xb, x2, x3);
+            sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(x0, x1));
+            sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
           };
           tc::tmem_ld32(tS, s);
           tc::tmem_wait_ld();
           if (ncol > 32) tc::tmem_ld32(tS + 32, s + 32);
+          if (diag || ncol < 32) mask(0, 32);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) eight(k);
+          for (int c = 0; c < 8; ++c) four(c);
           if (ncol > 32) tc::tmem_wait_ld();
           tc::fence_before();
           tc::mbar_arrive_warp(b_se + 8 * b);
+          // the second 32: all of them when nearly full, else in steps of 8
+          if (diag && ncol > 32)
+            mask(32, 64);
+          else if (ncol > 56)
+            mask(56, 64);
+          else if (ncol > 32 && (ncol & 7))
+            mask(32, 64);
+          if (ncol > 56) {
 #pragma unroll
-          for (int k = 4; k < 8; ++k) eight(k);
+            for (int c = 8; c < 16; ++c) four(c);
+          } else {
+#pragma unroll
+            for (int c = 8; c < 14; c += 2) {
+              if (4 * c >= ncol) break;
+              four(c);
+              four(c + 1);
+            }
+          }
           float v0, v1;
           tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), v0, v1);
-          const float v = v0 + v1, n = total + v, d = n - total;
-          rest += (total - (n - d)) + (v - d);
-          total = n;
+          const float v = v0 + v1, w = total + v, d = w - total;
+          rest += (total - (w - d)) + (v - d);
+          total = w;
         }
         if (!resident) tc::mbar_arrive_warp(b_qe + 8 * st);
       }
       if (h == 1) C.half[t][r] = total + rest;
       tc::bar_sync(1 + 4 * t + (warp & 3), 64);
-      if (h == 0 && key < e.n) {
+      if (h == 0 && key < n) {
         const float v = total + rest + C.half[t][r];
         if (e.mqs > 1) {
           A.part[e.mpart0 + ((int64_t)qs * A.hkv + head) * ((e.n + 3) & ~3ll) + key] = v;
