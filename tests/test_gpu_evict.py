@@ -81,6 +81,11 @@ def test_long_rows():
     check([150000], 140000, 4, 333, hkv=1, seed=5)
 
 
+def test_rows_longer_than_a_cluster_holds():
+    """450 000 tokens: the weights are read again in each pass."""
+    check([450000], 1000, 4, 333, hkv=1, kind="ties", seed=16)
+
+
 @pytest.mark.parametrize("dst_type", ["q4_0", "q8_0", "q5_1", "kvarn4", "kvarn3"])
 def test_quantized_destination(dst_type):
     check([900, 300, 20], 600, 4, 100, dst_type=dst_type, tail=128, seed=6)
