@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = __shfl_sync(FULL, C.tmem, 0);
+  asm volatile("griddepcontrol.launch_dependents;");  // (a join, which waits for this grid's end)
 
   if (warp >= NSOFT) {
     tc::regs_down<R_REST>();
@@ -552,55 +553,59 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   if (warp == W_MMA) tc::tmem_free(tm, 512);
 }
 
-// Joins the splits of a row (log-sum-exp, in split order): one warp per (query token, query head).
-__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ BArgs A, int64_t items) {
-  const int lane = threadIdx.x & 31, hq = A.hkv * A.G;
-  int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (it >= items) return;
+// Joins the splits of a row (log-sum-exp, in split order): a block per (query token, query head), a
+// thread per channel, all splits' loads in flight.  Set up behind the attention, waiting only for it.
+__global__ void __launch_bounds__(D) k_attn_join(const __grid_constant__ BArgs A) {
+  __shared__ float weight[MAXSPL];
+  __shared__ float total[2];
+  const int tid = threadIdx.x, hq = A.hkv * A.G;
+  int64_t it = blockIdx.x;
   int ei = 0;
   for (;; ++ei) {
     const int64_t c = A.e[ei].nsplit > 1 ? (int64_t)A.e[ei].nq * hq : 0;
     if (it < c) break;
     it -= c;
   }
-  const BEntry &e = A.e[ei];
-  const float *rec = A.part + (e.part0 + it * e.nsplit) * PREC;
-  float m[2], l[2], M = -INFINITY;
+  const int ns = A.e[ei].nsplit;
+  const float *rec = A.part + (A.e[ei].part0 + it * ns) * PREC;
+  const int64_t row = A.e[ei].q0 * hq + it;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid < 32) {
+    float m[2], l[2], M = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int k = lane + 32 * u;
-    m[u] = k < e.nsplit ? rec[(int64_t)k * PREC] : -INFINITY;
-    l[u] = k < e.nsplit ? rec[(int64_t)k * PREC + 1] : 0.f;
-    M = fmaxf(M, m[u]);
+    for (int u = 0; u < 2; ++u) {
+      const int k = tid + 32 * u;
+      m[u] = k < ns ? rec[(int64_t)k * PREC] : -INFINITY;
+      l[u] = k < ns ? rec[(int64_t)k * PREC + 1] : 0.f;
+      M = fmaxf(M, m[u]);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    float L = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float f = m[u] == -INFINITY ? 0.f : tc::ex2(m[u] - M);
+      weight[tid + 32 * u] = f;
+      L = fmaf(f, l[u], L);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+    if (tid == 0) {
+      total[0] = L;
+      if (A.lse) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+    }
   }
+  float v[16], a = 0.f;
+  for (int k0 = 0; k0 < ns; k0 += 16) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-  float f[2], L = 0.f;
+    for (int u = 0; u < 16; ++u) v[u] = k0 + u < ns ? rec[(int64_t)(k0 + u) * PREC + 4 + tid] : 0.f;
+    if (k0 == 0) __syncthreads();
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    f[u] = m[u] == -INFINITY ? 0.f : tc::ex2(m[u] - M);
-    L = fmaf(f[u], l[u], L);
+    for (int u = 0; u < 16; ++u)
+      if (k0 + u < ns) a = fmaf(weight[k0 + u], v[u], a);
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < e.nsplit; ++k) {
-    const float w = __shfl_sync(FULL, (k >> 5) ? f[1] : f[0], k & 31);
-    const float4 v = *reinterpret_cast<const float4 *>(rec + (int64_t)k * PREC + 4 + 4 * lane);
-    a[0] = fmaf(w, v.x, a[0]);
-    a[1] = fmaf(w, v.y, a[1]);
-    a[2] = fmaf(w, v.z, a[2]);
-    a[3] = fmaf(w, v.w, a[3]);
-  }
-  const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
-  const int64_t row = e.q0 * hq + it;
-  uint2 w;
-  if (A.io_f16)
-    w = make_uint2(tc::round2<true>(a[0] * inv, a[1] * inv), tc::round2<true>(a[2] * inv, a[3] * inv));
-  else
-    w = make_uint2(tc::round2<false>(a[0] * inv, a[1] * inv), tc::round2<false>(a[2] * inv, a[3] * inv));
-  *reinterpret_cast<uint2 *>(A.out + row * D + 4 * lane) = w;
-  if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2;
+  const float L = total[0], o = a * (L > 0.f ? 1.f / L : (L == L ? 0.f : L));
+  A.out[row * D + tid] = A.io_f16 ? __half_as_ushort(__float2half_rn(o)) : __bfloat16_as_ushort(__float2bfloat16_rn(o));
 }
 
 // ---- attention weights ------------------------------------------------------------------------------
@@ -692,6 +697,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = __shfl_sync(FULL, C.tmem, 0);
+  asm volatile("griddepcontrol.launch_dependents;");  // (a join, which waits for this grid's end)
   const int z0 = (e.slot * A.hkv + head) * A.src.sides;
 
   if (warp == W_LOAD) {
@@ -918,6 +924,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
 
 // Adds the splits of the query tiles, in order: one thread per (token, KV head).
 __global__ void __launch_bounds__(256) k_mass_join(const __grid_constant__ BArgs A, int64_t items) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (it >= items) return;
   int ei = 0;
@@ -940,73 +947,149 @@ __global__ void __launch_bounds__(256) k_q16(const uint4 *q, uint4 *dst, int64_t
   if (i < n) dst[i] = bf16x8_to_ring(q[i], 1);
 }
 
-// ---- quantized caches: one side's values rebuilt in the original basis as F16 rows --------------
-// One warp per (token, head); lane holds channels 4 lane .. 4 lane + 3.  Keys are kept as an F16
+// ---- quantized caches: values rebuilt in the original basis as F16 rows --------------------------
+// A warp takes four tokens of a (slot, head, side); a token belongs to eight lanes, 16 channels each
+// (lane part p: channels 4 p + 32 j + (0..3), j = 0..3: one 32-bit word of the stored planes per block).  Keys are kept as an F16
 // high part and the F16 remainder (22 bits: a score is an exponent, and the log-sum-exp and the
 // weights are fp32 results); values, whose result is rounded to 16 bits, as one F16.
+constexpr int MAXR = 128;  // slots per launch
 struct Rebuild {
-  int32_t seq, slot, which;
-  int64_t n, Q;
+  int32_t n, which;  // slots; side (2: K and V, by blockIdx.y)
+  int64_t cap;
+  int32_t first;     // slot of entry 0
+  struct {
+    int32_t seq, n, Q, block0;
+  } s[MAXR];
 };
+constexpr int RT = 32;  // tokens of a block (8 warps of 4)
 
 template <int FAM, int BITS>
-__global__ void __launch_bounds__(256) k_rebuild(LayerView L, Rebuild R, uint16_t *dst, int64_t cap) {
-  const int lane = threadIdx.x & 31;
-  const int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (it >= R.n * L.hkv) return;
-  const int head = (int)(it / R.n);
-  const int64_t p = it % R.n;
-  float v[4];
-  if (p >= R.Q) {
-    load4(reinterpret_cast<const uint16_t *>(ring_row(L, R.seq, head, R.which, p)) + 4 * lane, L.tail_f16, v);
+__global__ void __launch_bounds__(256) k_rebuild(LayerView L, const __grid_constant__ Rebuild R, uint16_t *dst) {
+  constexpr int WL = plane_lo(BITS), WH = plane_hi(BITS);
+  const int lane = threadIdx.x & 31, part = lane & 7;
+  int i = 0;
+  while (i + 1 < R.n && R.s[i + 1].block0 <= (int)blockIdx.x) ++i;
+  const int per = (R.s[i].n + RT - 1) / RT, local = blockIdx.x - R.s[i].block0;
+  const int head = local / per, p = local % per * RT + (threadIdx.x >> 5) * 4 + (lane >> 3);
+  const int seq = R.s[i].seq, which = R.which == 2 ? (int)blockIdx.y : R.which;
+  const bool on = p < R.s[i].n;
+  float v[16];  // channel 4 part + 32 j + k at 4 j + k
+  if (!on || p >= R.s[i].Q) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint2 w = make_uint2(0u, 0u);
+      if (on) w = *reinterpret_cast<const uint2 *>(ring_row(L, seq, head, which, p) + 32 * j + 4 * part);
+      const float2 a = ring2f(w.x, L.tail_f16), b = ring2f(w.y, L.tail_f16);
+      v[4 * j] = a.x, v[4 * j + 1] = a.y, v[4 * j + 2] = b.x, v[4 * j + 3] = b.y;
+    }
   } else {
     const SubLayout lay = sub_layout(FAM, BITS);
-    const uint8_t *sub = subpage_ptr(L, R.seq, p / GROUP, head, R.which);
-    const int tip = (int)(p % GROUP);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int ch = 4 * lane + e, blk = ch >> 5;
-      const uint32_t f = R.which == 0 ? k_field<BITS>(sub + tip * 16 * BITS, ch)
-                                      : v_field<BITS>(sub + (tip >> 2) * 64 * BITS, tip & 3, ch);
-      float x = (float)code_value<FAM, BITS>(f) * __half2float(reinterpret_cast<const __half *>(sub + lay.d)[tip * 4 + blk]);
-      if (FAM == FAM_ASYM) x += __half2float(reinterpret_cast<const __half *>(sub + lay.m)[tip * 4 + blk]);
-      if (FAM == FAM_KVARN) {
-        x *= __half2float(reinterpret_cast<const __half *>(sub + lay.t)[tip]);
-        x *= __half2float(reinterpret_cast<const __half *>(sub + lay.c)[ch]);
-      }
-      v[e] = x;
+    const uint8_t *sub = subpage_ptr(L, seq, p / GROUP, head, which);
+    const int tip = p % GROUP;
+    const uint2 d2 = *reinterpret_cast<const uint2 *>(sub + lay.d + 8 * tip);
+    const float2 d01 = __half22float2(*reinterpret_cast<const __half2 *>(&d2.x)),
+                 d23 = __half22float2(*reinterpret_cast<const __half2 *>(&d2.y));
+    const float d[4] = {d01.x, d01.y, d23.x, d23.y};
+    float m[4] = {0.f, 0.f, 0.f, 0.f}, t = 1.f;
+    if (FAM == FAM_ASYM) {
+      const uint2 m2 = *reinterpret_cast<const uint2 *>(sub + lay.m + 8 * tip);
+      const float2 m01 = __half22float2(*reinterpret_cast<const __half2 *>(&m2.x)),
+                   m23 = __half22float2(*reinterpret_cast<const __half2 *>(&m2.y));
+      m[0] = m01.x, m[1] = m01.y, m[2] = m23.x, m[3] = m23.y;
     }
-    if (FAM == FAM_KVARN) {
-      // H.x.kappa: stages 1, 2 inside the lane, 4 .. 64 across lanes
-      float a = v[0] + v[1], b = v[0] - v[1], c = v[2] + v[3], d = v[2] - v[3];
-      v[0] = a + c, v[2] = a - c, v[1] = b + d, v[3] = b - d;
+    if (FAM == FAM_KVARN) t = __half2float(reinterpret_cast<const __half *>(sub + lay.t)[tip]);
+    uint32_t f[16];
+    if (which == 0) {
+      // channels 32 j + 4 part + k: byte k of word (part / F, j) of each plane, field part % F
+      constexpr int FL = 8 / WL, FH = WH ? 8 / (WH ? WH : 1) : 1;
+      const uint8_t *tok = sub + tip * 16 * BITS;
+      const uint4 lo = *reinterpret_cast<const uint4 *>(tok + 16 * (part / FL));
+      uint4 hi = make_uint4(0u, 0u, 0u, 0u);
+      if (WH) hi = *reinterpret_cast<const uint4 *>(tok + 16 * WL + 16 * (part / FH));
+      const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-      for (int o = 1; o <= 16; o <<= 1) {
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float other = __shfl_xor_sync(FULL, v[e], o);
-          v[e] = (lane & o) ? other - v[e] : v[e] + other;
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x = (wl[j] >> (8 * k + (part % FL) * WL)) & ((1u << WL) - 1u);
+          if (WH) x |= ((wh[j] >> (8 * k + (part % FH) * WH)) & ((1u << WH) - 1u)) << WL;
+          f[4 * j + k] = x;
         }
+    } else {
+      // channel e = 4 part + k of block j: byte (token of the quad) of word e / F, field e % F
+      const uint8_t *quad = sub + (tip >> 2) * 64 * BITS;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[4 * j + k] = v_field<BITS>(quad, tip & 3, 32 * j + 4 * part + k);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float c[4] = {1.f, 1.f, 1.f, 1.f};
+      if (FAM == FAM_KVARN) {
+        const uint2 c2 = *reinterpret_cast<const uint2 *>(sub + lay.c + 2 * (32 * j + 4 * part));
+        const float2 c01 = __half22float2(*reinterpret_cast<const __half2 *>(&c2.x)),
+                     c23 = __half22float2(*reinterpret_cast<const __half2 *>(&c2.y));
+        c[0] = c01.x, c[1] = c01.y, c[2] = c23.x, c[3] = c23.y;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= kKappa();
+      for (int k = 0; k < 4; ++k) {
+        float x = (float)code_value<FAM, BITS>(f[4 * j + k]) * d[j];
+        if (FAM == FAM_ASYM) x += m[j];
+        if (FAM == FAM_KVARN) x = x * t * c[k];
+        v[4 * j + k] = x;
+      }
     }
   }
-  uint16_t *row = dst + ((((int64_t)R.slot * L.hkv + head) * 3 + 2 * R.which) * cap + p) * D + 4 * lane;
-  const __half2 h[2] = {__floats2half2_rn(v[0], v[1]), __floats2half2_rn(v[2], v[3])};
-  *reinterpret_cast<uint2 *>(row) = *reinterpret_cast<const uint2 *>(h);
-  if (R.which == 0) {
-    const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
-    const __half2 r[2] = {__floats2half2_rn(v[0] - a.x, v[1] - a.y), __floats2half2_rn(v[2] - b.x, v[3] - b.y)};
-    *reinterpret_cast<uint2 *>(row + cap * D) = *reinterpret_cast<const uint2 *>(r);
+  if (FAM == FAM_KVARN) {
+    // H.x.kappa of the quantized rows: stages 1 and 2 inside a word, 4 .. 16 over the eight lanes, 32
+    // and 64 over the blocks.  (Tail rows of a warp take part in the exchange and keep their own.)
+    float y[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) y[q] = v[q];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float *z = y + 4 * j;
+      const float a = z[0] + z[1], b = z[0] - z[1], c = z[2] + z[3], d = z[2] - z[3];
+      z[0] = a + c, z[2] = a - c, z[1] = b + d, z[3] = b - d;
+    }
+#pragma unroll
+    for (int o = 1; o <= 4; o <<= 1) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const float other = __shfl_xor_sync(FULL, y[q], o);
+        y[q] = (lane & o) ? other - y[q] : y[q] + other;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = y[k] + y[4 + k], b = y[k] - y[4 + k], c = y[8 + k] + y[12 + k], d = y[8 + k] - y[12 + k];
+      y[k] = a + c, y[8 + k] = a - c, y[4 + k] = b + d, y[12 + k] = b - d;
+    }
+    if (p < R.s[i].Q) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = y[q] * kKappa();
+    }
+  }
+  if (!on) return;
+  uint16_t *row = dst + ((((int64_t)(R.first + i) * L.hkv + head) * 3 + 2 * which) * R.cap + p) * D + 4 * part;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h[2] = {__floats2half2_rn(v[4 * j], v[4 * j + 1]), __floats2half2_rn(v[4 * j + 2], v[4 * j + 3])};
+    *reinterpret_cast<uint2 *>(row + 32 * j) = *reinterpret_cast<const uint2 *>(h);
+    if (which == 0) {
+      const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
+      const __half2 q[2] = {__floats2half2_rn(v[4 * j] - a.x, v[4 * j + 1] - a.y),
+                            __floats2half2_rn(v[4 * j + 2] - b.x, v[4 * j + 3] - b.y)};
+      *reinterpret_cast<uint2 *>(row + R.cap * D + 32 * j) = *reinterpret_cast<const uint2 *>(q);
+    }
   }
 }
 
-cudaError_t rebuild(int fam, int bits, const LayerView &L, const Rebuild &R, uint16_t *dst, int64_t cap,
+cudaError_t rebuild(int fam, int bits, const LayerView &L, const Rebuild &R, unsigned blocks, uint16_t *dst,
                     cudaStream_t st) {
-  const unsigned grid = (unsigned)((R.n * L.hkv + 7) / 8);
 #define KVQ_RB(F, B) \
-  if (fam == F && bits == B) { k_rebuild<F, B><<<grid, 256, 0, st>>>(L, R, dst, cap); return cudaGetLastError(); }
+  if (fam == F && bits == B) { k_rebuild<F, B><<<dim3(blocks, R.which == 2 ? 2 : 1), 256, 0, st>>>(L, R, dst); return cudaGetLastError(); }
   KVQ_RB(FAM_SYM, 2) KVQ_RB(FAM_SYM, 3) KVQ_RB(FAM_SYM, 4) KVQ_RB(FAM_SYM, 5) KVQ_RB(FAM_SYM, 6) KVQ_RB(FAM_SYM, 8)
   KVQ_RB(FAM_ASYM, 2) KVQ_RB(FAM_ASYM, 3) KVQ_RB(FAM_ASYM, 4) KVQ_RB(FAM_ASYM, 5) KVQ_RB(FAM_ASYM, 6)
   KVQ_RB(FAM_KVARN, 2) KVQ_RB(FAM_KVARN, 3) KVQ_RB(FAM_KVARN, 4) KVQ_RB(FAM_KVARN, 5) KVQ_RB(FAM_KVARN, 6)
@@ -1163,11 +1246,24 @@ int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, void 
   }
   uint16_t *dst = static_cast<uint16_t *>(workspace);
   *s = Source{dst, std::max<int64_t>(P.cap, 1), std::max(1, (int)P.slot_seq.size()), 1, 3};
-  for (size_t i = 0; i < P.slot_seq.size(); ++i) {
-    const int64_t n = c->len[(size_t)layer * c->p.n_seqs + P.slot_seq[i]];
-    for (int which = 0; which < (values ? 2 : 1); ++which) {
-      const Rebuild R{P.slot_seq[i], (int)i, which, n, quantized_len(c, n)};
-      if (rebuild(which ? c->fam_v : c->fam_k, which ? c->bits_v : c->bits_k, L, R, dst, P.cap, st) != cudaSuccess)
+  for (size_t base = 0; base < P.slot_seq.size(); base += MAXR) {
+    Rebuild R;
+    R.n = (int)std::min<size_t>(MAXR, P.slot_seq.size() - base);
+    R.cap = P.cap;
+    R.first = (int)base;
+    int64_t blocks = 0;
+    for (int i = 0; i < R.n; ++i) {
+      const int seq = P.slot_seq[base + i];
+      const int64_t n = c->len[(size_t)layer * c->p.n_seqs + seq];
+      R.s[i] = {seq, (int32_t)n, (int32_t)quantized_len(c, n), (int32_t)blocks};
+      blocks += (n + RT - 1) / RT * c->p.n_kv_heads;
+      if (blocks > INT32_MAX) return KVQ_E_UNSUPPORTED;
+    }
+    const bool both = values && c->p.type_k == c->p.type_v;
+    for (int which = 0; which < (values && !both ? 2 : 1); ++which) {
+      R.which = both ? 2 : which;
+      if (rebuild(which ? c->fam_v : c->fam_k, which ? c->bits_v : c->bits_k, L, R, (unsigned)blocks, dst, st) !=
+          cudaSuccess)
         return KVQ_E_CUDA;
       note_launches(1);
     }
@@ -1247,6 +1343,21 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
   if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return true;
+}
+
+// Launches a kernel that waits itself (griddepcontrol.wait) for the one in front of it.
+template <typename... P, typename... Q>
+bool launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t st, const Q &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1330,8 +1441,8 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
                                  : run_attn<false>(map, qmap, A, (unsigned)ctas, st))
       return rc;
     if (joins == 0) continue;
-    k_attn_join<<<(unsigned)((joins + 7) / 8), 256, 0, st>>>(A, joins);
-    if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
+    if (joins > INT32_MAX) return KVQ_E_UNSUPPORTED;
+    if (!launch_behind(k_attn_join, (unsigned)joins, D, st, A)) return KVQ_E_CUDA;
     note_launches(1);
   }
   return KVQ_OK;
@@ -1395,8 +1506,7 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
                                  : run_mass<false>(kmap, qmap, A, (unsigned)ctas, st))
       return rc;
     if (joins == 0) continue;
-    k_mass_join<<<(unsigned)((joins + 255) / 256), 256, 0, st>>>(A, joins);
-    if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
+    if (!launch_behind(k_mass_join, (unsigned)((joins + 255) / 256), 256, st, A, joins)) return KVQ_E_CUDA;
     note_launches(1);
   }
   return KVQ_OK;

@@ -5,11 +5,13 @@
 // of 10^7 leaves fp32 no correct digit of the fast pairs), then sin and cos are fp32; a rotation
 // is two fp32 multiplies and adds per pair and one rounding to the output type.
 //
-// Bound: HBM (each row read once, written once).  A block takes TT tokens: its threads first fill
-// a table of TT x 64 (cos, sin) in shared memory (64-bit work shared by all heads of a token), then
-// stream the rows, one thread per unit of 16 channels (8 pairs), in 16-byte pieces.
+// Bound: HBM (each row read once, written once).  A block takes tt tokens: its threads fill a table
+// of tt x 64 (cos, sin) in shared memory (64-bit work shared by all heads of a token), then stream the
+// rows in pieces of 16 bytes, two to a thread and step, asked for before the table is made.
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "kvq_internal.h"
 
@@ -52,141 +54,235 @@ struct Elem<KVQ_DT_F16> {
   static __device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
 };
 
-// 8 consecutive elements (16-byte aligned) as fp32, and back
+// A unit of a head: two pieces of E elements, 16 bytes each as they are read (E = 4 for fp32, 8 for
+// the 16-bit types), a head being 64 / E units.  Consecutive lanes take consecutive pieces.
 template <int T>
-__device__ __forceinline__ void load8(const typename Elem<T>::type *p, float (&x)[8]) {
-  using E = typename Elem<T>::type;
-  if constexpr (T == KVQ_DT_F32) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+constexpr int E_OF = T == KVQ_DT_F32 ? 4 : 8;
+
+// Where the two pieces of unit u lie: pairs E u .. of the halves (E u, half + E u); adjacent pairs: the
+// pieces u of each half of the head; behind the rotating ones, pieces of the channels that pass through.
+template <int E>
+__device__ __forceinline__ void places(int u, int half, int adjacent, int &a, int &b) {
+  if (adjacent) {
+    a = E * u;
+    b = 64 + E * u;
+  } else if (E * u < half) {
+    a = E * u;
+    b = half + E * u;
   } else {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const E *e = reinterpret_cast<const E *>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = Elem<T>::up(e[i]);
-  }
-}
-template <int T>
-__device__ __forceinline__ void store8(typename Elem<T>::type *p, const float (&x)[8]) {
-  using E = typename Elem<T>::type;
-  if constexpr (T == KVQ_DT_F32) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    uint4 v;
-    E *e = reinterpret_cast<E *>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = Elem<T>::down(x[i]);
-    *reinterpret_cast<uint4 *>(p) = v;
+    a = 2 * half + (E * u - half);
+    b = a + (64 - half);
   }
 }
 
-// One unit u (0..7) of a head: 8 pairs of 16 channels.  VEC (rot_dim a multiple of 16): whole
-// 16-byte pieces; the units behind the rotating ones carry the channels that pass through.
-// Otherwise pairs straddle the pieces and are moved one by one.
-template <int TI, int TO, bool VEC>
-__device__ __forceinline__ void turn_unit(const typename Elem<TI>::type *x, typename Elem<TO>::type *y, int u,
-                                          int half, int adjacent, const float2 *cs) {
-  if constexpr (VEC) {
-    const int rot = 2 * half;
-    int ca, cb;
-    if (adjacent) {
-      ca = 16 * u, cb = ca + 8;
-    } else if (8 * u < half) {
-      ca = 8 * u, cb = half + 8 * u;
-    } else {
-      ca = rot + 16 * (u - half / 8), cb = ca + 8;
-    }
-    if (TI == TO && 8 * u >= half) {  // channels that pass through keep their bits (NaN payloads too)
-      constexpr int V = sizeof(typename Elem<TI>::type) / 2;
-      uint4 w[2 * V];
+// elements 2 i and 2 i + 1 of a piece, as fp32; and back
+template <int T>
+__device__ __forceinline__ float2 get2(const uint4 &w, int i) {
+  if constexpr (T == KVQ_DT_F32) return i ? make_float2(__uint_as_float(w.z), __uint_as_float(w.w))
+                                          : make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+  return ring2f(i == 0 ? w.x : (i == 1 ? w.y : (i == 2 ? w.z : w.w)), T == KVQ_DT_F16);
+}
+template <int T>
+__device__ __forceinline__ uint32_t round_pair(float x, float y) {
+  if constexpr (T == KVQ_DT_F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// N consecutive fp32 values to a piece of type T
+template <int T, int N>
+__device__ __forceinline__ void put(typename Elem<T>::type *y, const float (&x)[N]) {
+  if constexpr (T == KVQ_DT_F32) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        w[j] = reinterpret_cast<const uint4 *>(x + ca)[j];
-        w[V + j] = reinterpret_cast<const uint4 *>(x + cb)[j];
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        reinterpret_cast<uint4 *>(y + ca)[j] = w[j];
-        reinterpret_cast<uint4 *>(y + cb)[j] = w[V + j];
-      }
-      return;
-    }
-    float a[8], b[8];
-    load8<TI>(x + ca, a);
-    load8<TI>(x + cb, b);
-    if (8 * u >= half) {
-      // converted only
-    } else if (adjacent) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 t = cs[8 * u + j], v = cs[8 * u + 4 + j];
-        const float p = a[2 * j], r = a[2 * j + 1], m = b[2 * j], n = b[2 * j + 1];
-        a[2 * j] = p * t.x - r * t.y;
-        a[2 * j + 1] = r * t.x + p * t.y;
-        b[2 * j] = m * v.x - n * v.y;
-        b[2 * j + 1] = n * v.x + m * v.y;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 t = cs[8 * u + j];
-        const float p = a[j], r = b[j];
-        a[j] = p * t.x - r * t.y;
-        b[j] = r * t.x + p * t.y;
-      }
-    }
-    store8<TO>(y + ca, a);
-    store8<TO>(y + cb, b);
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(y + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else if constexpr (N == 4) {
+    *reinterpret_cast<uint2 *>(y) = make_uint2(round_pair<T>(x[0], x[1]), round_pair<T>(x[2], x[3]));
   } else {
-#pragma unroll 1
-    for (int j = 0; j < 8; ++j) {
-      const int i = 8 * u + j;
-      const bool on = i < half;
-      const int ca = adjacent ? 2 * i : (on ? i : i + half), cb = adjacent ? ca + 1 : (on ? i + half : ca + 64 - half);
-      if (TI == TO && !on) {
-        const typename Elem<TI>::type xa = x[ca], xb = x[cb];
-        reinterpret_cast<typename Elem<TI>::type *>(y)[ca] = xa;
-        reinterpret_cast<typename Elem<TI>::type *>(y)[cb] = xb;
-        continue;
-      }
-      const float p = Elem<TI>::up(x[ca]), r = Elem<TI>::up(x[cb]);
-      const float2 t = on ? cs[i] : make_float2(1.f, 0.f);
-      y[ca] = Elem<TO>::down(on ? p * t.x - r * t.y : p);
-      y[cb] = Elem<TO>::down(on ? r * t.x + p * t.y : r);
-    }
+    *reinterpret_cast<uint4 *>(y) = make_uint4(round_pair<T>(x[0], x[1]), round_pair<T>(x[2], x[3]),
+                                               round_pair<T>(x[4], x[5]), round_pair<T>(x[6], x[7]));
   }
 }
+
+// The angles of one token: the cosine of pair p at float cos_at(p), its sine 64 floats behind, in an
+// order in which the lanes of a head read 128 consecutive bytes at once (pair by pair they met in four
+// banks: 88 us for 16384 tokens of 48 heads in BF16).
+__device__ __forceinline__ int cos_at(int pair) { return 32 * ((pair >> 2) & 1) + 4 * (pair >> 3) + (pair & 3); }
+constexpr int TAB = 128;  // floats per token
+
+// Rotates the unit (wa, wb) whose pieces lie at channels a and b and stores it.  Channels that pass
+// through keep their bits where the types agree (NaN payloads too).
+template <int TI, int TO>
+__device__ __forceinline__ void turn(const uint4 &wa, const uint4 &wb, typename Elem<TO>::type *y, int a, int b,
+                                     int half, int adjacent, const float *cs) {
+  constexpr int E = E_OF<TI>;
+  float xa[E], xb[E];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 p = get2<TI>(wa, i), r = get2<TI>(wb, i);
+    xa[2 * i] = p.x, xa[2 * i + 1] = p.y, xb[2 * i] = r.x, xb[2 * i + 1] = r.y;
+  }
+  if (adjacent) {
+    auto piece = [&](float (&x)[E], int at, const uint4 &w) {
+      if (at >= 2 * half) {
+        if constexpr (TI == TO)
+          *reinterpret_cast<uint4 *>(y + at) = w;
+        else
+          put<TO, E>(y + at, x);
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float c = cs[cos_at(at / 2) + i], s = cs[64 + cos_at(at / 2) + i];
+        const float p = x[2 * i], r = x[2 * i + 1];
+        x[2 * i] = p * c - r * s;
+        x[2 * i + 1] = r * c + p * s;
+      }
+      put<TO, E>(y + at, x);
+    };
+    piece(xa, a, wa);
+    piece(xb, b, wb);
+    return;
+  }
+  if (a >= 2 * half) {
+    if constexpr (TI == TO) {
+      *reinterpret_cast<uint4 *>(y + a) = wa;
+      *reinterpret_cast<uint4 *>(y + b) = wb;
+    } else {
+      put<TO, E>(y + a, xa);
+      put<TO, E>(y + b, xb);
+    }
+    return;
+  }
+#pragma unroll
+  for (int g = 0; g < E / 4; ++g) {
+    const float4 c4 = *reinterpret_cast<const float4 *>(cs + cos_at(a + 4 * g));
+    const float4 s4 = *reinterpret_cast<const float4 *>(cs + 64 + cos_at(a + 4 * g));
+    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = xa[4 * g + j], r = xb[4 * g + j];
+      xa[4 * g + j] = p * c[j] - r * s[j];
+      xb[4 * g + j] = r * c[j] + p * s[j];
+    }
+  }
+  put<TO, E>(y + a, xa);
+  put<TO, E>(y + b, xb);
+}
+
+// rot_dim no multiple of 16: pairs straddle the pieces and are moved one by one
+template <int TI, int TO>
+__device__ __forceinline__ void turn_pairs(const typename Elem<TI>::type *x, typename Elem<TO>::type *y, int u,
+                                           int half, int adjacent, const float *cs) {
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    const int i = 8 * u + j;
+    const bool on = i < half;
+    const int ca = adjacent ? 2 * i : (on ? i : i + half), cb = adjacent ? ca + 1 : (on ? i + half : ca + 64 - half);
+    if constexpr (TI == TO) {
+      if (!on) {
+        const typename Elem<TI>::type xa = x[ca], xb = x[cb];
+        y[ca] = xa;
+        y[cb] = xb;
+        continue;
+      }
+    }
+    const float p = Elem<TI>::up(x[ca]), r = Elem<TI>::up(x[cb]);
+    const float2 t = on ? make_float2(cs[cos_at(i)], cs[64 + cos_at(i)]) : make_float2(1.f, 0.f);
+    y[ca] = Elem<TO>::down(on ? p * t.x - r * t.y : p);
+    y[cb] = Elem<TO>::down(on ? r * t.x + p * t.y : r);
+  }
+}
+
+// units in flight per thread
+constexpr int UNITS = 3;
 
 template <int TQI, int TQO, bool VEC>
 __global__ void __launch_bounds__(NT) k_rope(const __grid_constant__ RopeArgs A) {
-  extern __shared__ float2 cs[];  // [tt][64]
-  const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * A.tt;
-  const int nt = (int)min((int64_t)A.tt, A.n - t0);
-  for (int e = tid; e < nt * 64; e += NT) {
-    const int i = e & 63;
-    if (i >= A.half) continue;
-    // half turns, reduced to [-1, 1]: exact after the one 64-bit product
-    const double a = (double)A.pos[A.axis[i] * A.pos_ld + t0 + (e >> 6)] * A.f[i];
-    float s, c;
-    sincospif((float)(a - 2.0 * rint(0.5 * a)), &s, &c);
-    cs[e] = make_float2(c, A.sign * s);
-  }
-  __syncthreads();
-  const int units = 8 * (A.hq + A.hk);
+  extern __shared__ __align__(16) float tables[];  // [2][tt][TAB]
   using EI = typename Elem<TQI>::type;
   using EO = typename Elem<TQO>::type;
-  for (int e = tid; e < nt * units; e += NT) {
-    const int tl = e / units, r = e - tl * units, h = r >> 3, u = r & 7;
-    const int64_t t = t0 + tl;
-    if (h < A.hq)
-      turn_unit<TQI, TQO, VEC>(static_cast<const EI *>(A.q) + t * A.q_ld + h * D,
-                               static_cast<EO *>(A.qo) + t * A.qo_ld + h * D, u, A.half, A.adjacent, cs + 64 * tl);
-    else
-      turn_unit<KVQ_DT_BF16, KVQ_DT_BF16, VEC>(
-          static_cast<const __nv_bfloat16 *>(A.k) + t * A.k_ld + (h - A.hq) * D,
-          static_cast<__nv_bfloat16 *>(A.ko) + t * A.ko_ld + (h - A.hq) * D, u, A.half, A.adjacent, cs + 64 * tl);
+  constexpr int KT = KVQ_DT_BF16;
+  const int tid = threadIdx.x;
+  constexpr int EQ = E_OF<TQI>, PQ = 64 / EQ;  // units of a q head; a k head has 8
+  const int nq = PQ * A.hq, units = VEC ? nq + 8 * A.hk : 8 * (A.hq + A.hk);
+  // this thread's pair, the same for every token: its frequency and axis are read once per block
+  const int pair = tid & 63;
+  const double freq = pair < A.half ? A.f[pair] : 0.0;
+  const int32_t *pos = A.pos + (pair < A.half ? A.axis[pair] : 0) * A.pos_ld;
+  int odd = 0;
+#pragma unroll 1
+  for (int64_t t0 = (int64_t)blockIdx.x * A.tt; t0 < A.n; t0 += (int64_t)gridDim.x * A.tt, odd ^= 1) {
+    const int nt = (int)min((int64_t)A.tt, A.n - t0), all = nt * units;
+    float *cs = tables + odd * A.tt * TAB;  // (the other one may still be in use)
+    auto table = [&]() {
+      for (int j = tid >> 6; j < nt; j += NT / 64) {
+        // half turns, reduced to [-1, 1]: exact after the one 64-bit product
+        const double a = (double)pos[t0 + j] * freq;
+        float s, c;
+        sincospif((float)(a - 2.0 * rint(0.5 * a)), &s, &c);
+        cs[TAB * j + cos_at(pair)] = c;
+        cs[TAB * j + 64 + cos_at(pair)] = A.sign * s;
+      }
+      __syncthreads();
+    };
+    if constexpr (VEC) {
+      // U units a thread, all on their way before the table is made (one round: tt is chosen so)
+      constexpr int U = UNITS;
+      bool made = false;
+#pragma unroll 1
+      for (int e0 = 0; e0 < all; e0 += U * NT) {
+        uint4 wa[U], wb[U];
+        int tl[U], at[U], a[U], b[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const int e = e0 + j * NT + tid;
+          if (e >= all) break;
+          tl[j] = e / units;
+          at[j] = e - tl[j] * units;
+          if (at[j] < nq) {
+            places<EQ>(at[j] % PQ, A.half, A.adjacent, a[j], b[j]);
+            const EI *p = static_cast<const EI *>(A.q) + (t0 + tl[j]) * A.q_ld + at[j] / PQ * D;
+            wa[j] = *reinterpret_cast<const uint4 *>(p + a[j]);
+            wb[j] = *reinterpret_cast<const uint4 *>(p + b[j]);
+          } else {
+            const int k = at[j] - nq;
+            places<8>(k & 7, A.half, A.adjacent, a[j], b[j]);
+            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(A.k) + (t0 + tl[j]) * A.k_ld + (k >> 3) * D;
+            wa[j] = *reinterpret_cast<const uint4 *>(p + a[j]);
+            wb[j] = *reinterpret_cast<const uint4 *>(p + b[j]);
+          }
+        }
+        if (!made) table();
+        made = true;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          if (e0 + j * NT + tid >= all) break;
+          const float *c = cs + TAB * tl[j];
+          if (at[j] < nq)
+            turn<TQI, TQO>(wa[j], wb[j], static_cast<EO *>(A.qo) + (t0 + tl[j]) * A.qo_ld + at[j] / PQ * D, a[j], b[j],
+                           A.half, A.adjacent, c);
+          else
+            turn<KT, KT>(wa[j], wb[j],
+                         static_cast<__nv_bfloat16 *>(A.ko) + (t0 + tl[j]) * A.ko_ld + ((at[j] - nq) >> 3) * D, a[j],
+                         b[j], A.half, A.adjacent, c);
+        }
+      }
+    } else {
+      table();
+      for (int e = tid; e < all; e += NT) {
+        const int tl = e / units, r = e - tl * units, h = r >> 3, u = r & 7;
+        const int64_t t = t0 + tl;
+        if (h < A.hq)
+          turn_pairs<TQI, TQO>(static_cast<const EI *>(A.q) + t * A.q_ld + h * D,
+                               static_cast<EO *>(A.qo) + t * A.qo_ld + h * D, u, A.half, A.adjacent, cs + TAB * tl);
+        else
+          turn_pairs<KT, KT>(static_cast<const __nv_bfloat16 *>(A.k) + t * A.k_ld + (h - A.hq) * D,
+                             static_cast<__nv_bfloat16 *>(A.ko) + t * A.ko_ld + (h - A.hq) * D, u, A.half, A.adjacent,
+                             cs + TAB * tl);
+      }
+    }
   }
 }
 
@@ -275,10 +371,11 @@ extern "C" int kvq_rope(const kvq_rope_params *p, const double *inv_freq, int64_
   A.half = half;
   A.adjacent = p->adjacent;
   A.sign = p->inverse ? -1.f : 1.f;
-  // few tokens: a block each (latency); many: four to a block, whose 256 angles are one per thread
-  A.tt = n_tokens >= 4096 ? 4 : 1;
-  const unsigned grid = (unsigned)((n_tokens + A.tt - 1) / A.tt);
-  const size_t smem = sizeof(float2) * 64 * A.tt;
+  // a block takes the tokens whose units its threads hold at once; fewer tokens than blocks: one each
+  const int64_t units = (n_q_heads && q_type == KVQ_DT_F32 ? 16ll : 8ll) * n_q_heads + 8ll * n_k_heads, held = UNITS * NT;
+  A.tt = (int)std::max<int64_t>(1, std::min<int64_t>({held / units, n_tokens / (4 * 148), 32}));
+  const unsigned grid = (unsigned)std::min<int64_t>((n_tokens + A.tt - 1) / A.tt, 148 * 6);
+  const size_t smem = sizeof(float) * 2 * TAB * A.tt;
   const bool vec = p->rot_dim % 16 == 0;
   const int qi = n_q_heads ? q_type : KVQ_DT_BF16, qo = n_q_heads ? q_out_type : KVQ_DT_BF16;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
