@@ -664,6 +664,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
     return max(qs * e.mqc, A.causal && i > 0 ? (int)(i / TB) : 0);
   };
   const int f0 = first_tile(p0);
+  if (f0 >= qb && e.mqs > 1) return;  // no query of the split sees the group (the join leaves it out)
   const bool resident = qb - f0 <= NQS;
   const bool lo = A.src.sides == 3;
   const uint32_t q0s = base + NKS * TILE;
@@ -935,8 +936,11 @@ __global__ void __launch_bounds__(256) k_mass_join(const __grid_constant__ BArgs
   }
   const BEntry &e = A.e[ei];
   const int64_t head = it / e.n, t = it % e.n, ld = (e.n + 3) & ~3ll;
+  // splits of which no query sees the group of t hold nothing
+  const int64_t i = t / (2 * BT) / e.mpairs * e.mpairs * 2 * BT - (e.n - e.nq);
   float v = 0.f;
-  for (int k = 0; k < e.mqs; ++k) v += A.part[e.mpart0 + (k * A.hkv + head) * ld + t];
+  for (int k = A.causal && i > 0 ? (int)(i / e.mtb) / e.mqc : 0; k < e.mqs; ++k)
+    v += A.part[e.mpart0 + (k * A.hkv + head) * ld + t];
   const int64_t at = ((int64_t)e.out * A.hkv + head) * A.mass_ld + t;
   A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
 }
@@ -1163,7 +1167,7 @@ void plan_mass(BEntry *e, int ne, int hkv, int G, int sms, int64_t *floats) {
     most = std::max(most, np);
     heavy |= qt > NQS;
   }
-  const int64_t target = std::min<int64_t>(64, std::max<int64_t>(8, units / (8 * sms)));
+  const int64_t target = std::min<int64_t>(64, std::max<int64_t>(8, units / (6 * sms)));
   int64_t lo = 1, hi = most;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;

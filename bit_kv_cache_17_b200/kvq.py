@@ -405,6 +405,7 @@ class KVCache:
         self._t16 = torch.float16 if self.params.tail_f16 else torch.bfloat16
         self._raw_stream = _raw_stream_of(torch)
         self._size = _sz()
+        self._rows16 = {}  # layer -> view
         self._size_ref = C.byref(self._size)
         self._ws = None
         self._ws_bytes = {}  # (n_seqs, n_q_heads) -> kvq_workspace_bytes
@@ -473,15 +474,18 @@ class KVCache:
     def rows16(self, layer):
         """The 16-bit rows of a layer, a view of the storage [n_seqs, n_kv_heads, 2 (K, V), ring rows, 128]
         in the tail's type: token p of a sequence in row p mod the ring rows."""
-        torch, p = self.torch, self.params
-        kvarn = any(8 <= t <= 13 or (p.var_norm and t != 0) for t in (p.type_k, p.type_v))
-        rows = p.max_ctx if p.type_k == 0 else p.tail + (256 if kvarn else 0)
-        if rows == 0:
-            _refuse("rows16", "a cache without a 16-bit tail")
-        off, _ = kvq_locate(self.handle, 1, layer, 0, 0, 0, 0, 0)
-        n = p.n_seqs * p.n_kv_heads * 2 * rows * 128
-        x = self.storage[off:off + 2 * n].view(torch.float16 if p.tail_f16 else torch.bfloat16)
-        return x.view(p.n_seqs, p.n_kv_heads, 2, rows, 128)
+        x = self._rows16.get(layer)
+        if x is None:
+            torch, p = self.torch, self.params
+            kvarn = any(8 <= t <= 13 or (p.var_norm and t != 0) for t in (p.type_k, p.type_v))
+            rows = p.max_ctx if p.type_k == 0 else p.tail + (256 if kvarn else 0)
+            if rows == 0:
+                _refuse("rows16", "a cache without a 16-bit tail")
+            off, _ = kvq_locate(self.handle, 1, layer, 0, 0, 0, 0, 0)
+            n = p.n_seqs * p.n_kv_heads * 2 * rows * 128
+            x = self.storage[off:off + 2 * n].view(self._t16).view(p.n_seqs, p.n_kv_heads, 2, rows, 128)
+            self._rows16[layer] = x
+        return x
 
     def _elsewhere(self, stream):
         """Whether a stream or device other than the current one has to be made current (_on)."""
