@@ -91,16 +91,17 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 constexpr int BT = 128;            // rows of a query tile, tokens of a key tile
 constexpr int NSOFT = 16;          // softmax warps
 constexpr int W_MMA = 16, W_LOAD = 17;
-// Five warpgroups: four of softmax, one of which the load and the MMA warp use two warps.  Launched
-// with 96 registers a thread (61440 in all): 4 x 128 x 104 + 128 x 64 = 61440.
-constexpr int NT = 640;
-constexpr int R_SOFT = 104, R_REST = 64;
+// 16 of softmax, one that issues the products, one that loads; 96 registers a thread either way
+// (register splits between the warpgroups measured the same)
+constexpr int NT = 576;
 constexpr int TILE = BT * D * 2;   // bytes of a tile
 constexpr int HALF = TILE / 2;     // 64 channels of it
 constexpr int MAXST = 6;           // stages
 constexpr float TAU = 8.f;         // lazy maximum, log2 units
 constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
 constexpr int MAXSPL = 64;
+constexpr int EXG = BT * 129 + 2 * BT;  // floats a group leaves in the stages at the end (rows padded to 129)
+static_assert(2 * EXG * 4 <= 5 * TILE, "two groups' rows fit the stages");
 constexpr int EMU = 0x10;
 
 struct Ctl {
@@ -109,6 +110,9 @@ struct Ctl {
   uint32_t tmem;
   int32_t abort;
   float row[2][2][BT];  // [group][half][row]: maxima, then sums
+  // what the end of the kernel needs of the launch, so that no register holds it across the tiles
+  int64_t q0, part0;
+  int32_t tok0, tok1, head, sp, nsplit, halves, nt;
 };
 constexpr int OFF_CTL = 7 * TILE;  // two or one query tiles and five or six stages
 constexpr int ATTN_SMEM = OFF_CTL + (int)sizeof(Ctl);
@@ -131,7 +135,8 @@ struct Ring {
   }
 };
 
-template <bool F16>
+// LO: the keys have remainders (a rebuilt cache)
+template <bool F16, bool LO>
 __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
                                                 const __grid_constant__ CUtensorMap qmap,
                                                 const __grid_constant__ BArgs A) {
@@ -143,6 +148,11 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   }
   Ctl &C = *reinterpret_cast<Ctl *>(S + OFF_CTL);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
+  if (warp == W_LOAD && lane == 0) {
+    tc::prefetch_map(&qmap);
+    tc::prefetch_map(&map);
+  }
+  if (warp == W_MMA) tc::tmem_alloc(tc::smem_u32(&C.tmem), 512);
   int ei = 0;
   while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
   const BEntry &e = A.e[ei];
@@ -158,14 +168,15 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   const int j0 = sp * e.cps, nt = max(0, min(e.cps, kt - j0));
   const int nst = halves ? 6 : 5;
   const uint32_t stage0 = base + ntile * TILE;
-  const bool lo = A.src.sides == 3;
+  constexpr bool lo = LO;
+  constexpr int sides = LO ? 3 : 2;
   const uint32_t cb = tc::smem_u32(&C);
   const uint32_t b_full = cb + (uint32_t)offsetof(Ctl, full), b_empty = cb + (uint32_t)offsetof(Ctl, empty);
   const uint32_t b_s = cb + (uint32_t)offsetof(Ctl, s_full), b_p = cb + (uint32_t)offsetof(Ctl, p_full);
   const uint32_t b_o = cb + (uint32_t)offsetof(Ctl, o_full), b_tmp = cb + (uint32_t)offsetof(Ctl, tmp);
   const uint32_t b_q = cb + (uint32_t)offsetof(Ctl, q_full);
   volatile int32_t *abort = &C.abort;
-  const int z0 = (e.slot * A.hkv + head) * A.src.sides, zv = z0 + A.src.sides - 1;
+  const int z0 = (e.slot * A.hkv + head) * sides, zv = z0 + sides - 1;
 
   if (warp == W_LOAD && lane == 0) {
     for (int i = 0; i < MAXST; ++i) {
@@ -192,14 +203,10 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       tc::tma_load3(stage0 + HALF, &map, 64, j0 * BT, z0, b_full);
     }
   }
-  if (warp == W_MMA) tc::tmem_alloc(cb + (uint32_t)offsetof(Ctl, tmem), 512);
-  // rows of a tile that no copy writes
-  for (int u = tid; u < ntile * (BT - TB * G) * 16; u += NT) {
-    const int t = u / ((BT - TB * G) * 16), v = u % ((BT - TB * G) * 16);
-    *reinterpret_cast<uint4 *>(S + t * TILE + (v & 1) * HALF + (TB * G + (v >> 4)) * 128 + ((v >> 1) & 7) * 16) =
-        make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) {
+    C.q0 = e.q0, C.part0 = e.part0;
+    C.tok0 = tok0, C.tok1 = tok1, C.head = head, C.sp = sp, C.nsplit = e.nsplit, C.halves = halves, C.nt = nt;
   }
-  tc::fence_async_smem();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -207,7 +214,6 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   asm volatile("griddepcontrol.launch_dependents;");  // (a join, which waits for this grid's end)
 
   if (warp >= NSOFT) {
-    tc::regs_down<R_REST>();
     if (warp == W_LOAD) {
       // ---- K and V tiles in the order they are used: two tiles K0 V0 K1 V1 ..; halves K0 K1 V0 K2 V1 ..
       int n_issued = 0;
@@ -358,27 +364,26 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       tc::mbar_wait(b_o, 0, abort, A.status, false);
     }
   } else {
-    tc::regs_up<R_SOFT>();
     // ---- softmax: row r of query tile t (halves: of the one tile), tokens 64 h .. 64 h + 63 of a tile
     const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tm + lanes + BT * t + 64 * h, tO = tm + lanes + 2 * BT + D * t + 64 * h;
     const int pair = 1 + 4 * t + (warp & 3);  // barrier of the two warps that share these rows
-    const int i = tok0 + (halves ? 0 : t * TB) + r / G;
-    const bool on = r < TB * G && i < tok1;
-    // (rows that hold no query see everything: a mask for them would hold up their warp on every tile)
-    const int64_t lim = on ? limit_of(A, e, i) : e.n;
-    const int step = halves ? 2 : 1;
+    // (rows that hold no query see everything, a mask for them would hold up their warp on every tile, and
+    // never move the maximum: the products of what lies behind the queries in shared memory are anything)
+    const bool live = r < TB * G;
+    const int row_tok = tok0 + (halves ? 0 : t * TB) + r / G;
+    // visible tokens from this thread's half of the group's first tile on; tiles of the group
+    int left = (int)(live && row_tok < tok1 ? limit_of(A, e, row_tok) : e.n) - (j0 + (halves ? t : 0)) * BT - 64 * h;
+    const int count = halves ? (nt + 1 - t) >> 1 : nt, stride = halves ? 2 * BT : BT;
     float m = -INFINITY, l = 0.f;
-    int u = 0;
 #pragma unroll 1
-    for (int j = halves ? t : 0; j < nt; j += step, ++u) {
-      const int64_t left = lim - (int64_t)(j0 + j) * BT - 64 * h;  // visible tokens of this half tile
+    for (int u = 0; u < count; ++u, left -= stride) {
       tc::mbar_wait(b_s + 8 * t, u & 1, abort, A.status);
       tc::fence_after();
-      float s[64], mx[8];
+      float s[64], mx[4];
 #pragma unroll
-      for (int v = 0; v < 8; ++v) mx[v] = -INFINITY;
+      for (int v = 0; v < 4; ++v) mx[v] = -INFINITY;
       // the first 32 are searched for their maximum while the others are read
       tc::tmem_ld32(tS, s);
 #pragma unroll
@@ -386,20 +391,18 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         tc::tmem_wait_ld();
         if (c == 0) tc::tmem_ld32(tS + 32, s + 32);
         if (left < 64) {
-          const int lv = (int)max((int64_t)0, left);
 #pragma unroll
           for (int v = 0; v < 32; ++v)
-            if (32 * c + v >= lv) s[32 * c + v] = -INFINITY;
+            if (32 * c + v >= left) s[32 * c + v] = -INFINITY;
         }
 #pragma unroll
-        for (int v = 0; v < 32; v += 16) {
+        for (int v = 0; v < 32; v += 8) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[32 * c + v + k]), s[32 * c + v + 8 + k]);
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[32 * c + v + k]), s[32 * c + v + 4 + k]);
         }
       }
-      const float top =
-          fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
-          A.qscale;
+      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.qscale;
+      if (!live) top = -INFINITY;
       if (tc::bar_any(pair, 64, top > m + TAU)) {
         // a row's first scores, or some far above the maximum in use: both threads take the new one
         C.row[t][h][r] = top;
@@ -413,13 +416,13 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         }
         if (u > 0 && __any_sync(FULL, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float o[32];
-            tc::tmem_ld32(tO + 32 * c, o);
+          for (int c = 0; c < 64; c += 16) {  // (the scores are held meanwhile: few registers are left)
+            uint32_t o[16];
+            tc::tmem_ld16(tO + c, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int v = 0; v < 32; ++v) o[v] *= alpha;
-            tc::tmem_st32(tO + 32 * c, reinterpret_cast<const uint32_t *>(o));
+            for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+            tc::tmem_st16(tO + c, o);
           }
           tc::tmem_wait_st();
           tc::fence_before();
@@ -458,14 +461,15 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     C.row[t][h][r] = l;
     tc::bar_sync(pair, 64);
     l = C.row[t][0][r] + C.row[t][1][r];
-    if (nt > 0) {
+    const int tiles = C.nt;
+    if (tiles > 0) {
       tc::mbar_wait(b_o, 0, abort, A.status);
       tc::fence_after();
     }
     // halves: group 1 leaves its own in the stages (all consumed), group 0 joins the two
-    float *ex = reinterpret_cast<float *>(S + TILE);  // [128 rows][129], then m and l
-    const bool any1 = halves && nt > 1;
-    if (any1 && t == 1) {
+    const bool one = C.halves, join = one && tiles > 1, split = C.nsplit > 1;
+    float *ex = reinterpret_cast<float *>(S + (one ? 1 : 2) * TILE);  // [128 rows][129], then m and l
+    if (join && t == 1) {
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         float o[32];
@@ -479,10 +483,10 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         ex[128 * 129 + 2 * r + 1] = l;
       }
     }
-    if (any1) tc::bar_sync(9, 32 * NSOFT);
-    if (!(halves && t == 1)) {
+    if (join) tc::bar_sync(9, 32 * NSOFT);
+    if (!(one && t == 1)) {
       float f0 = 1.f, f1 = 0.f;
-      if (any1) {
+      if (join) {
         const float m1 = ex[128 * 129 + 2 * r], l1 = ex[128 * 129 + 2 * r + 1];
         const float mn = fmaxf(m, m1);
         f0 = m == -INFINITY ? 0.f : tc::ex2(m - mn);
@@ -490,14 +494,15 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         m = mn;
         l = l * f0 + l1 * f1;
       }
-      const int64_t row = (e.q0 + i) * hq + head * G + r % G;
-      const bool split = e.nsplit > 1;
+      // a split's rows in fp32, behind what the other group left; otherwise through the query tile (no
+      // product reads it any more), in its layout
       const float inv = split ? 1.f : (l > 0.f ? 1.f / l : (l == l ? 0.f : l));
-      float *rec = split ? A.part + (e.part0 + ((int64_t)i * hq + head * G + r % G) * e.nsplit + sp) * PREC : nullptr;
+      float *part = ex + (one ? 1 : t) * EXG;
+      uint8_t *qt = S + t * TILE;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         float o[32];
-        if (nt > 0) {
+        if (tiles > 0) {
           tc::tmem_ld32(tO + 32 * c, o);
           tc::tmem_wait_ld();
         } else {
@@ -505,17 +510,15 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
           for (int v = 0; v < 32; ++v) o[v] = 0.f;
         }
         const int ch = 64 * h + 32 * c;
-        if (any1) {
+        if (join) {
 #pragma unroll
           for (int v = 0; v < 32; ++v) o[v] = o[v] * f0 + ex[r * 129 + ch + v] * f1;
         }
-        if (on && split) {
+        if (split) {
 #pragma unroll
-          for (int v = 0; v < 32; v += 4)
-            *reinterpret_cast<float4 *>(rec + 4 + ch + v) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
-        } else if (!split) {
-          // through the query tile (no product reads it any more), in its layout
-          uint8_t *dst = S + t * TILE + h * HALF + r * 128;
+          for (int v = 0; v < 32; ++v) part[r * 129 + ch + v] = o[v];
+        } else {
+          uint8_t *dst = qt + h * HALF + r * 128;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint32_t w[4];
@@ -527,23 +530,31 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
           }
         }
       }
-      if (!split) {
-        // whole rows to memory, two per warp and instruction
-        tc::bar_sync(10 + t, 256);
-        const uint8_t *src = S + t * TILE;
-        const int rows = min(TB, tok1 - tok0 - (halves ? 0 : t * TB)) * G;  // (below 0: none)
+      // whole rows to memory, 512 or 256 bytes at once
+      tc::bar_sync(10 + t, 256);
+      const int first = C.tok0 + (one ? 0 : t * TB), rows = min(TB, C.tok1 - first) * G;  // (below 0: none)
+      const int head0 = C.head * G, ns = C.nsplit;
+      if (split) {
+        float *rec0 = A.part + (C.part0 + (int64_t)C.sp) * PREC;
+        for (int rr = (tid & 255) >> 5; rr < rows; rr += 8) {
+          const float *v = part + rr * 129 + 4 * lane;
+          *reinterpret_cast<float4 *>(rec0 + ((int64_t)(first + rr / G) * hq + head0 + rr % G) * ns * PREC + 4 + 4 * lane) =
+              make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (h == 0 && r < rows) {
+          float *rec = rec0 + ((int64_t)(first + r / G) * hq + head0 + r % G) * ns * PREC;
+          rec[0] = m;
+          rec[1] = l;
+        }
+      } else {
         for (int p = tid & 255; p < rows * 16; p += 256) {
           const int rr = p >> 4, c = p & 15;
-          const int64_t at = (e.q0 + tok0 + (halves ? 0 : t * TB) + rr / G) * hq + head * G + rr % G;
+          const int64_t at = (C.q0 + first + rr / G) * hq + head0 + rr % G;
           *reinterpret_cast<uint4 *>(A.out + at * D + 8 * c) =
-              *reinterpret_cast<const uint4 *>(src + (c >> 3) * HALF + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
+              *reinterpret_cast<const uint4 *>(qt + (c >> 3) * HALF + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
         }
-      }
-      if (on && split && h == 0) {
-        rec[0] = m;
-        rec[1] = l;
-      } else if (on && A.lse && h == 0) {
-        A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        if (A.lse && h == 0 && r < rows)
+          A.lse[(C.q0 + first + r / G) * hq + head0 + r % G] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
       }
     }
   }
@@ -1366,11 +1377,11 @@ bool launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, cudaStre
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <bool F16>
+template <bool F16, bool LO>
 int run_attn(const CUtensorMap &map, const CUtensorMap &qmap, const BArgs &A, unsigned ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(k_attn<F16>, ATTN_SMEM, done)) return KVQ_E_CUDA;
-  k_attn<F16><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
+  if (!allow_smem(k_attn<F16, LO>, ATTN_SMEM, done)) return KVQ_E_CUDA;
+  k_attn<F16, LO><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
   if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
   note_launches(1);
   return KVQ_OK;
@@ -1441,9 +1452,8 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
     }
     if (ctas == 0) continue;
     if (ctas > INT32_MAX) return KVQ_E_UNSUPPORTED;
-    if (const int rc = A.src.f16 ? run_attn<true>(map, qmap, A, (unsigned)ctas, st)
-                                 : run_attn<false>(map, qmap, A, (unsigned)ctas, st))
-      return rc;
+    const auto run = A.src.sides == 3 ? run_attn<true, true> : (A.src.f16 ? run_attn<true, false> : run_attn<false, false>);
+    if (const int rc = run(map, qmap, A, (unsigned)ctas, st)) return rc;
     if (joins == 0) continue;
     if (joins > INT32_MAX) return KVQ_E_UNSUPPORTED;
     if (!launch_behind(k_attn_join, (unsigned)joins, D, st, A)) return KVQ_E_CUDA;
