@@ -192,12 +192,12 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     tc::fence_mbar_init();
     // the query tiles and the first keys are on their way while the rest is set up.  A tile takes
     // whatever rows follow an entry's last one too: rows do not mix, and those are never written out
-    const uint32_t bytes = 2 * TB * G * 128;
-    tc::mbar_expect(b_q, ntile * bytes);
-    for (int t = 0; t < ntile; ++t)
-      for (int h = 0; h < 2; ++h)
-        tc::tma_load4(base + t * TILE + h * HALF, &qmap, 64 * h, 0, head, (int)(e.q0 + tok0 + t * TB), b_q);
+    // (a CTA without key tiles asks for nothing: its zeros pass through the same shared memory)
     if (nt > 0) {
+      tc::mbar_expect(b_q, ntile * 2 * TB * G * 128);
+      for (int t = 0; t < ntile; ++t)
+        for (int h = 0; h < 2; ++h)
+          tc::tma_load4(base + t * TILE + h * HALF, &qmap, 64 * h, 0, head, (int)(e.q0 + tok0 + t * TB), b_q);
       tc::mbar_expect(b_full, TILE);
       tc::tma_load3(stage0, &map, 0, j0 * BT, z0, b_full);
       tc::tma_load3(stage0 + HALF, &map, 64, j0 * BT, z0, b_full);
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       // no copy is in flight when the CTA ends (its pipeline may have been given up)
       for (int i = max(0, n_issued - nst); i < n_issued; ++i)
         tc::mbar_wait(b_full + 8 * (i % nst), (i / nst) & 1, abort, A.status, false);
-      tc::mbar_wait(b_q, 0, abort, A.status, false);
+      if (nt > 0) tc::mbar_wait(b_q, 0, abort, A.status, false);
     } else if (warp == W_MMA && nt > 0) {
       // ---- products: the whole warp waits (its values stay in uniform registers), one lane issues
       constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0), idO = tc::idesc(F16, BT, D, 1);

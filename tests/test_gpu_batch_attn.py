@@ -71,6 +71,21 @@ def test_more_entries_than_a_launch_takes():
     run_case("bf16", lens, [1 + i % 3 for i in range(70)], 1, 2, False, seed=8)
 
 
+def test_empty_sequences_give_zeros_every_time():
+    """Rows of empty sequences beside others, many at once and again and again: exactly zero (their
+    query rows must never show through)."""
+    t = P.torch()
+    lens = [0] * 12 + [300]
+    k, v = P.kv(4, lens, 2)
+    c = P.cache("bf16", lens, 2, k, v)
+    n_q = [100] * 13
+    q = P.queries(4, 1300, 10, t.bfloat16)
+    for _ in range(20):
+        out, lse = c.batch_attn(0, list(range(13)), n_q, q, return_lse=True)
+        assert bool((out[:1200] == 0).all()) and bool((lse[:1200] == -math.inf).all())
+        assert bool((out[1200:] != 0).any())
+
+
 def test_sharp_and_shifted_scores():
     """Scores far apart (the weights of all but a few tokens vanish) and far from zero."""
     run_case("bf16", [1000], [33], 2, 5, False, seed=9, qscale=16.0)
