@@ -30,7 +30,6 @@ struct BEntry {
   int32_t nblk;     // blocks of query tokens
   int32_t nsplit;   // splits of the key tiles
   int32_t cps;      // key tiles per split
-  int32_t halves;   // one query tile: the two softmax groups take the even and the odd key tiles
   int32_t cta0;     // first CTA
   int64_t part0;    // first partial record (nsplit > 1)
   int32_t mgroup;   // weights: groups of key pairs per KV head,
@@ -79,8 +78,8 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //  - a load warp fetches 128-token K and V tiles (32 KB each) with TMA into a ring of stages;
 //  - one thread issues S = Q.K^T (M = N = 128, SS) and O += P.V (P from tensor memory, V as the
 //    MN-major operand straight from the rows), S, P and O in tensor memory: 512 columns;
-//  - two softmax groups of eight warps: group t owns query tile t (two tiles), or the key tiles j = t
-//    mod 2 (one tile: `halves`, joined in shared memory at the end).  A row of a group belongs to two
+//  - two softmax groups of eight warps: group t owns query tile t, or, in a block of one tile, the key
+//    tiles j = t mod 2 (`halves`, joined in shared memory at the end).  A row of a group belongs to two
 //    threads, 64 of the tile's tokens each (one thread per row left the warps waiting on their own
 //    instructions: 810 us for a causal 8k prompt of 40 heads).  While one group works on its scores
 //    the tensor core runs the other's products; a half of P is handed over as soon as it is written.
@@ -160,9 +159,9 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   const int local = blockIdx.x - e.cta0;
   const int sp = local % e.nsplit, head = local / e.nsplit % A.hkv;
   const int blk = e.nblk - 1 - local / e.nsplit / A.hkv;  // the last (causal: longest) first
-  const bool halves = e.halves;
+  const int tok0 = blk * 2 * TB, tok1 = min(e.nq, tok0 + 2 * TB);
+  const bool halves = tok1 - tok0 <= TB;
   const int ntile = halves ? 1 : 2;  // query tiles
-  const int tok0 = blk * ntile * TB, tok1 = min(e.nq, tok0 + ntile * TB);
   const int64_t lim_max = limit_of(A, e, tok1 - 1);
   const int kt = (int)((lim_max + BT - 1) / BT);
   const int j0 = sp * e.cps, nt = max(0, min(e.cps, kt - j0));
@@ -623,11 +622,11 @@ __global__ void __launch_bounds__(D) k_attn_join(const __grid_constant__ BArgs A
 //
 // mass[t] = sum over query rows r of 2^(x[t, r] - lse2[r]): with the lse given, one product and one
 // exponential per (token, row), no second pass.  The product is taken the other way round, S^T = K.Q^T
-// (tokens are the MMA's rows), so that a thread owns a token and its sum never leaves the thread: no
-// shuffles, no atomics, the order of the sum fixed by the tiles.
+// (tokens are the MMA's rows), so that a sum stays in its thread (two per token, half of the columns
+// each): no shuffles, no atomics, the order of the sum fixed by the tiles.
 //
 // One CTA per (entry, KV head, group of key-tile pairs, split of the query tiles): the two key tiles of
-// a pair belong to the two groups of four warps and share each query tile.  Up to three query tiles
+// a pair belong to the two groups of eight warps and share each query tile.  Up to three query tiles
 // stay in shared memory while the keys stream past (a window of queries: each key is read once, HBM
 // bound); more of them stream for each pair (a prompt: bound by the exponentials, 16 a cycle and SM).
 // Query tiles come by TMA as [token][head] rows of 64 channels, the tokens spread evenly over the
@@ -636,7 +635,7 @@ constexpr int NKS = 4, NQS = 3;  // key and query stages
 constexpr int OFF_MCTL = (NKS + NQS) * TILE;
 
 struct MCtl {
-  uint64_t k_full[NKS], k_empty[NKS], q_full[NQS], q_empty[NQS], s_full[4], s_empty[4], tmp, last;
+  uint64_t k_full[NKS], k_empty[NKS], q_full[NQS], q_empty[NQS], s_full[4], s_empty[4], last;
   alignas(16) float nlse[NQS][BT];  // -lse * log2(e) of the tile's rows
   float half[2][BT];                // sums of the second half of the columns
   uint32_t tmem;
@@ -683,7 +682,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   const uint32_t b_kf = cb + (uint32_t)offsetof(MCtl, k_full), b_ke = cb + (uint32_t)offsetof(MCtl, k_empty);
   const uint32_t b_qf = cb + (uint32_t)offsetof(MCtl, q_full), b_qe = cb + (uint32_t)offsetof(MCtl, q_empty);
   const uint32_t b_sf = cb + (uint32_t)offsetof(MCtl, s_full), b_se = cb + (uint32_t)offsetof(MCtl, s_empty);
-  const uint32_t b_tmp = cb + (uint32_t)offsetof(MCtl, tmp), b_last = cb + (uint32_t)offsetof(MCtl, last);
+  const uint32_t b_last = cb + (uint32_t)offsetof(MCtl, last);
   volatile int32_t *abort = &C.abort;
 
   if (warp == W_LOAD && lane == 0) {
@@ -699,7 +698,6 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
       tc::mbar_init(b_sf + 8 * i, 1);
       tc::mbar_init(b_se + 8 * i, 8);
     }
-    tc::mbar_init(b_tmp, 1);
     tc::mbar_init(b_last, 1);
     C.abort = 0;
     tc::fence_mbar_init();
@@ -1133,9 +1131,7 @@ void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
   const int TB = BT / G;
   int64_t blocks = 0, most = 1;
   for (int i = 0; i < ne; ++i) {
-    const int64_t tiles = ((int64_t)e[i].nq + TB - 1) / TB;
-    e[i].halves = tiles <= 1;
-    e[i].nblk = (int)(tiles <= 1 ? tiles : (tiles + 1) / 2);
+    e[i].nblk = (int)(((int64_t)e[i].nq + 2 * TB - 1) / (2 * TB));
     blocks += (int64_t)e[i].nblk * hkv;
     if (e[i].nblk) most = std::max(most, (e[i].n + BT - 1) / BT);
   }

@@ -310,16 +310,15 @@ class Rope:
                                            sections=sections + [0] * (4 - len(sections)), turns=int(turns),
                                            adjacent=int(adjacent), inverse=i, theta=float(theta)) for i in (0, 1)]
         self._ref = [C.byref(p) for p in self._p]
-        self._freq = None
-        if inv_freq is not None:
-            f = [float(x) for x in inv_freq]
-            if len(f) != rot_dim // 2:
-                _refuse("Rope", "inv_freq holds rot_dim / 2 values")
-            self._freq = (C.c_double * len(f))(*f)
+        # the host checks of the parameters, once: a call over no tokens
+        kvq_rope(self._p[0], None, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        half = rot_dim // 2
+        f = [theta ** (-2.0 * i / rot_dim) for i in range(half)] if inv_freq is None else [float(x) for x in inv_freq]
+        if len(f) != half:
+            _refuse("Rope", "inv_freq holds rot_dim / 2 values")
+        self._freq = (C.c_double * half)(*f)
         self._raw_stream = _raw_stream_of(torch)
         self._types = {torch.float32: KVQ_DT_F32, torch.bfloat16: KVQ_DT_BF16, torch.float16: KVQ_DT_F16}
-        # the host checks of the parameters, once: a call over no tokens
-        kvq_rope(self._p[0], self._freq, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
 
     @staticmethod
     def _rows(x, n, dev, name):
