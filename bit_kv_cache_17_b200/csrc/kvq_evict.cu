@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(NT) k_select(const __grid_constant__ EvictArgs
     if ((above >> lane & 1u) || ((equal >> lane & 1u) && ties < need)) {
       const uint32_t at = na + __popc(above & below) + min(ties, need);
       kept[at] = i0 + i + lane;
-      if (out) out[at] = mass[i + lane];
     }
     na += __popc(above);
     ne += __popc(equal);
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(NT) k_select(const __grid_constant__ EvictArgs
   cl.sync();  // (no CTA's shared memory goes while another reads it)
 }
 
-// Eight kept tokens of a head per warp: K rows in lanes 0..15, V rows in lanes 16..31.
+// Eight kept tokens of a head per warp, their weights and rows: K in lanes 0..15, V in lanes 16..31.
 // stage_k / stage_v: [row][hkv][128] BF16 for a destination that is appended to; otherwise the rows
 // go to the destination's ring.  (Rows of a BF16 cache never wrap.)
 constexpr int GR = 8;
@@ -244,6 +243,10 @@ __global__ void __launch_bounds__(256) k_gather(LayerView S, LayerView T, const 
   const int head = (int)(it / per), first = (int)(it % per) * GR, rows = min(GR, s.count - first);
   const int32_t *kept = A.kept + ((int64_t)(A.entry0 + e) * A.hkv + head) * A.budget + first;
   const int idx = lane < rows ? kept[lane] : 0;
+  if (A.mass_out && lane < rows) {
+    const int64_t r = (int64_t)(A.entry0 + e) * A.hkv + head;
+    A.mass_out[r * A.out_ld + first + lane] = __ldg(A.mass + r * A.mass_ld + idx);
+  }
   const uint4 *src = reinterpret_cast<const uint4 *>(
       S.ring + (((int64_t)s.src * S.hkv + head) * 2 + which) * S.ring_cap * (2 * D)) + part;
   uint4 v[GR];
