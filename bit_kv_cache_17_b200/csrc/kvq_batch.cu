@@ -636,6 +636,7 @@ constexpr int OFF_MCTL = (NKS + NQS) * TILE;
 
 struct MCtl {
   uint64_t k_full[NKS], k_empty[NKS], q_full[NQS], q_empty[NQS], s_full[4], s_empty[4], last;
+  uint64_t h_full[8], h_free[8];    // half sums of a warp's 32 keys: written, read
   alignas(16) float nlse[NQS][BT];  // -lse * log2(e) of the tile's rows
   float half[2][BT];                // sums of the second half of the columns
   uint32_t tmem;
@@ -682,6 +683,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   const uint32_t b_kf = cb + (uint32_t)offsetof(MCtl, k_full), b_ke = cb + (uint32_t)offsetof(MCtl, k_empty);
   const uint32_t b_qf = cb + (uint32_t)offsetof(MCtl, q_full), b_qe = cb + (uint32_t)offsetof(MCtl, q_empty);
   const uint32_t b_sf = cb + (uint32_t)offsetof(MCtl, s_full), b_se = cb + (uint32_t)offsetof(MCtl, s_empty);
+  const uint32_t b_hf = cb + (uint32_t)offsetof(MCtl, h_full), b_he = cb + (uint32_t)offsetof(MCtl, h_free);
   const uint32_t b_last = cb + (uint32_t)offsetof(MCtl, last);
   volatile int32_t *abort = &C.abort;
 
@@ -697,6 +699,10 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(b_sf + 8 * i, 1);
       tc::mbar_init(b_se + 8 * i, 8);
+    }
+    for (int i = 0; i < 8; ++i) {
+      tc::mbar_init(b_hf + 8 * i, 1);
+      tc::mbar_init(b_he + 8 * i, 1);
     }
     tc::mbar_init(b_last, 1);
     C.abort = 0;
@@ -912,18 +918,25 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
         }
         if (!resident) tc::mbar_arrive_warp(b_qe + 8 * st);
       }
-      if (h == 1) C.half[t][r] = total + rest;
-      tc::bar_sync(1 + 4 * t + (warp & 3), 64);
-      if (h == 0 && key < n) {
+      // the second half hands its sum over and goes on, the first one writes
+      const uint32_t hb = 8 * (4 * t + (warp & 3));
+      if (h == 1) {
+        if (p > p0) tc::mbar_wait(b_he + hb, (p - p0 - 1) & 1, abort, A.status);
+        C.half[t][r] = total + rest;
+        tc::mbar_arrive_warp(b_hf + hb);
+      } else {
+        tc::mbar_wait(b_hf + hb, (p - p0) & 1, abort, A.status);
         const float v = total + rest + C.half[t][r];
-        if (e.mqs > 1) {
-          A.part[e.mpart0 + ((int64_t)qs * A.hkv + head) * ((e.n + 3) & ~3ll) + key] = v;
-        } else {
-          const int64_t at = ((int64_t)e.out * A.hkv + head) * A.mass_ld + key;
-          A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
+        tc::mbar_arrive_warp(b_he + hb);
+        if (key < n) {
+          if (e.mqs > 1) {
+            A.part[e.mpart0 + ((int64_t)qs * A.hkv + head) * ((e.n + 3) & ~3ll) + key] = v;
+          } else {
+            const int64_t at = ((int64_t)e.out * A.hkv + head) * A.mass_ld + key;
+            A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
+          }
         }
       }
-      tc::bar_sync(1 + 4 * t + (warp & 3), 64);  // (the half sum is read before the next one is written)
     }
   }
   tc::fence_before();
