@@ -774,7 +774,6 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
     for (int i = max(0, qc - NQS); i < qc; ++i)
       tc::mbar_wait(b_qf + 8 * (i % NQS), (i / NQS) & 1, abort, A.status, false);
   } else if (warp == W_MMA) {
-    constexpr uint32_t idS = tc::idesc(F16, BT, BT, 0);
     const uint64_t dk = tc::desc_sw128(base, 0), dq = tc::desc_sw128(q0s, 0);
     const bool leader = tc::elect_one();
     Ring gk, gq;
@@ -798,6 +797,8 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
         tc::mbar_wait(b_qf + 8 * st, resident ? 0u : gq.phase, abort, A.status);
         if (!resident) gq.next(NQS);
         const uint64_t q = dq + (uint64_t)(st * (TILE >> 4));
+        // (as many columns as the tile's queries need, in steps of 16)
+        const uint32_t idS = tc::idesc(F16, BT, (min(TB, e.nq - a * TB) * G + 15) / 16 * 16, 0);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= nk) break;
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
           // the tile's columns in two halves of a multiple of 8; this thread's are [0, ncol) of its half,
           // those below c0 are queries in front of the token (causal)
           const int tok = a * TB, nc = min(TB, nq - tok) * G, hc = (nc + 15) / 16 * 8;
-          const int ncol = h ? nc - hc : hc;
+          const int ncol = h ? nc - hc : min(hc, nc);
           const bool diag = causal && tile0 + BT - 1 - past > tok;
           const int c0 = diag ? min(max(key - past - tok, 0), BT) * G - h * hc : 0;
           const uint32_t b = 2 * t + (sc & 1), tS = tm + lanes + BT * b + h * hc;

@@ -90,6 +90,23 @@ def test_decay_zero_reads_nothing_and_default_output():
     assert bool(((d - e).abs() <= 1e-5 * (1 + e)).all()) and bool(t.isfinite(d).all())
 
 
+@pytest.mark.parametrize("m", [1, 3, 26, 30])
+def test_an_entry_does_not_see_the_queries_behind_its_own(m):
+    """NaN queries of the next entry share a tile's copy with this entry's last ones."""
+    t = P.torch()
+    lens = [300, 300]
+    k, v = P.kv(5, lens, 1)
+    c = P.cache("bf16", lens, 1, k, v)
+    q = P.queries(5, m + 40, 5, t.bfloat16)
+    out, lse = c.batch_attn(0, [0, 1], [m, 40], q, return_lse=True)
+    want = c.attn_mass(0, [0, 1], [m, 40], q, lse)
+    q[m:] = math.nan
+    out2 = c.batch_attn(0, [0, 1], [m, 40], q)
+    got = c.attn_mass(0, [0, 1], [m, 40], q, lse)
+    assert t.equal(out2[:m], out[:m]) and t.equal(got[0], want[0])
+    assert bool(t.isnan(got[1]).all()) and bool(t.isnan(out2[m:]).all())
+
+
 def test_no_queries_only_decays():
     t = P.torch()
     k, v = P.kv(1, [50], 2)
