@@ -235,8 +235,9 @@ int kvq_locate(const kvq_cache *c, int32_t kind, int32_t layer, int32_t seq, int
  *    wrong, the cache buffer having been corrupted);
  *  - a decode merge ticket that was not zero when the decode began (a corrupted ticket, or
  *    two decodes of one cache overlapping on the GPU): that decode's output may be stale;
- *  - a wait between the roles of the chunk-attention kernel that ran out (each is bounded):
- *    that call's output is wrong; the kernel still finishes and frees what it holds. */
+ *  - a wait between the roles of a chunk-attention, batch-attention or attention-weight kernel
+ *    that ran out (each is bounded): that call's output is wrong; the kernel still finishes and
+ *    frees what it holds. */
 int kvq_get_status(kvq_cache *c, kvq_stream_t stream);
 
 /* Human-readable description of the cache (types, tail, bytes); valid until the next
@@ -320,12 +321,16 @@ int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs,
  * q: device [sum(n_q), n_q_heads, 128] in the cache's 16-bit format (BF16, or F16 with tail_f16),
  * the rows of entry 0 first; out: same shape and type; lse: device fp32 [sum(n_q), n_q_heads] or
  * NULL: log of the sum of exp(scale q.k) of each row.  softmax_scale <= 0 selects 1/sqrt(128).
- * A row that sees no token gives zeros and lse = -inf.  workspace: device, >=
- * kvq_batch_workspace_bytes.  Scores, the softmax and both sums are fp32; the weights are rounded to
- * the 16-bit type of the matrix product.  A BF16 cache (either tail format) is read as it is; the
- * values of a quantized cache are first rebuilt in the original basis in F16, in the workspace
- * (values and queries must then lie within the F16 range).  kvq_decode_attn remains the call for
- * one fp32 query row per quantized sequence. */
+ * A row that sees no token gives zeros and lse = -inf.  Cached values must be finite (a value that is
+ * not reaches every row that attends to its 128-token tile, also where the row does not see it).
+ * workspace: device, >= kvq_batch_workspace_bytes (NULL where that is 0); calls that may overlap on
+ * the GPU need workspaces of their own, and may otherwise run at the same time, the cache being only
+ * read.  Scores, the softmax and both sums are fp32; the weights are rounded to the 16-bit type of the
+ * matrix product.  A BF16 cache (either tail format) is read as it is; a quantized cache is first
+ * rebuilt in the original basis in the workspace, keys as F16 high part and remainder, values as F16
+ * (values and queries must then lie within the F16 range).  kvq_decode_attn remains the call for one
+ * fp32 query row per quantized sequence.  Results do not depend on what else runs: every sum has a
+ * fixed order. */
 int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids, const int32_t *n_q,
                    int32_t n_q_heads, int32_t causal, const void *q, float softmax_scale, void *out, float *lse,
                    void *workspace, size_t ws_bytes, kvq_stream_t stream);
