@@ -87,6 +87,9 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //    rescaled in tensor memory then), so most tiles need no correction and the two threads of a row
 //    only agree, by one barrier with an OR, that none is due.
 // Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
+// Bound, many rows: the chain scores -> maximum -> exponentials -> weights of a tile against the other
+// group's products (causal 8k prompt of 40 heads, F16: 577 us, 1190 TFLOP/s; tensor pipe 53 %, exponentials
+// 48 %).  Bound, one row: HBM (65 536 tokens, 268 MB: 48 us + the join, 5.0 TB/s).
 constexpr int BT = 128;            // rows of a query tile, tokens of a key tile
 constexpr int NSOFT = 16;          // softmax warps
 constexpr int W_MMA = 16, W_LOAD = 17;
@@ -101,6 +104,8 @@ constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, ac
 constexpr int MAXSPL = 64;
 constexpr int EXG = BT * 129 + 2 * BT;  // floats a group leaves in the stages at the end (rows padded to 129)
 static_assert(2 * EXG * 4 <= 5 * TILE, "two groups' rows fit the stages");
+// which of eight score pairs are exponentiated on the FMA pipe: one (causal 8k prompt of 40 heads: 577 us;
+// none 587, two 581 to 584)
 constexpr int EMU = 0x10;
 
 struct Ctl {
@@ -631,6 +636,8 @@ __global__ void __launch_bounds__(D) k_attn_join(const __grid_constant__ BArgs A
 // bound); more of them stream for each pair (a prompt: bound by the exponentials, 16 a cycle and SM).
 // Query tiles come by TMA as [token][head] rows of 64 channels, the tokens spread evenly over the
 // tiles; only the columns that hold queries are exponentiated, in steps of 8.
+// 32 queries over 65 536 tokens: 45 us (134 MB; exponentials and products take turns); every query of
+// prompts of 4096 and 512 tokens: 152 us (exponential unit 65 % busy).
 constexpr int NKS = 4, NQS = 3;  // key and query stages
 constexpr int OFF_MCTL = (NKS + NQS) * TILE;
 
@@ -643,6 +650,9 @@ struct MCtl {
   int32_t abort;
 };
 constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl);
+
+// which of four groups of columns have half of theirs exponentiated on the FMA pipe: one (weights of a
+// 4k prompt: 152 us; none 156, two 154)
 constexpr int MEMU = 0x1;
 static_assert(MASS_SMEM <= 232448, "shared memory per CTA");
 
@@ -976,9 +986,10 @@ __global__ void __launch_bounds__(256) k_q16(const uint4 *q, uint4 *dst, int64_t
 
 // ---- quantized caches: values rebuilt in the original basis as F16 rows --------------------------
 // A warp takes four tokens of a (slot, head, side); a token belongs to eight lanes, 16 channels each
-// (lane part p: channels 4 p + 32 j + (0..3), j = 0..3: one 32-bit word of the stored planes per block).  Keys are kept as an F16
-// high part and the F16 remainder (22 bits: a score is an exponent, and the log-sum-exp and the
-// weights are fp32 results); values, whose result is rounded to 16 bits, as one F16.
+// (lane part p: channels 4 p + 32 j + (0..3), j = 0..3: one 32-bit word of the stored planes per
+// block).  Keys are kept as an F16 high part and the F16 remainder (22 bits: a score is an exponent, and
+// the log-sum-exp and the weights are fp32 results); values, whose result is rounded to 16 bits, as one F16.  Bound: the stores
+// (9.2 k tokens of 8 heads, q8_0, K and V in one launch: 18 us for 72 MB written, 20 MB read).
 constexpr int MAXR = 128;  // slots per launch
 struct Rebuild {
   int32_t n, which;  // slots; side (2: K and V, by blockIdx.y)
@@ -1138,10 +1149,12 @@ struct Plan {
   size_t rebuilt_bytes = 0, part_bytes = 0, q16_bytes = 0, bytes = 0;
 };
 
-// Blocks and key splits of up to MAXE entries: without splits when there is a block for every SM;
-// otherwise the fewest key tiles per CTA (at least MIN_CPS: a join costs a launch) that one wave holds.
+// Blocks and key splits of up to MAXE entries: without splits when there is a block for every SM, or
+// no context is longer than four key tiles (one row over 512 tokens: 10.4 us either way, and one launch
+// less to issue); otherwise the fewest key tiles per CTA that one wave holds, down to one: the join, set
+// up behind the attention, costs less than a tile (one row over 1024 / 2048 / 4096 tokens: 10.3 / 10.3 /
+// 12.4 us with splits of one tile and more, 13.1 / 13.9 / 14.3 us with at least four).
 void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
-  constexpr int MIN_CPS = 4;
   const int TB = BT / G;
   int64_t blocks = 0, most = 1;
   for (int i = 0; i < ne; ++i) {
@@ -1155,8 +1168,8 @@ void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
     return n;
   };
   int64_t cps = most;
-  if (blocks < sms) {
-    int64_t lo = std::max<int64_t>(MIN_CPS, (most + MAXSPL - 1) / MAXSPL), hi = std::max(most, lo);
+  if (blocks < sms && most > 4) {
+    int64_t lo = (most + MAXSPL - 1) / MAXSPL, hi = std::max(most, lo);
     while (lo < hi) {
       const int64_t mid = (lo + hi) / 2;
       if (ctas(mid) <= sms) hi = mid; else lo = mid + 1;
@@ -1176,8 +1189,8 @@ void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
 }
 
 // Groups of key pairs and splits of the query tiles.  Up to three query tiles: they stay in shared
-// memory, and one wave of CTAs streams the keys.  More: items of about an eighth of an SM's share,
-// so that the causal ones even out.
+// memory, and one wave of CTAs streams the keys.  More: items of about a sixth of an SM's share, so
+// that the causal ones even out (4k prompt: a third 156 us, a fifth 150, an eighth 151, a twelfth 162).
 void plan_mass(BEntry *e, int ne, int hkv, int G, int sms, int64_t *floats) {
   const int TB = BT / G;
   int64_t units = 0, most = 1;

@@ -7,10 +7,11 @@
 // result is a function of the input alone.
 // A cluster of up to 8 CTAs takes a row: each keeps the keys of a contiguous segment in shared memory
 // (one read of the weights), the histograms and counts are added up through distributed shared memory.
-// Bound: instructions and the latency of the five visits to a segment, not the 4 bytes a token.
+// Bound: instructions and the latency of the five visits to a segment, not the 4 bytes a token
+// (128 rows of up to 32 768: 28 us; 8 rows of 2048: 8.5 us).
 // Compaction: the kept rows of K and V are copied to the destination's ring in order (a BF16
 // destination), or to the workspace and appended from there (a quantized one).  Bound: HBM; a warp has
-// eight rows of K and V in flight.
+// eight rows of K and V in flight (one row: 167 us for 16 x 4096 tokens of 8 heads; eight: 95 us, 5.6 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -412,7 +413,8 @@ extern "C" int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int3
       longest = std::max<int64_t>(longest, A.s[i].n);
     }
     // a CTA for every 2048 tokens, up to a cluster of 8, as long as the rows leave two places an SM for
-    // them (more CTAs only wait for each other's cluster barriers), or shared memory holds no more
+    // them (128 rows of 32 768: one CTA a row 83 us, two 56, four 59, in an earlier form), or while
+    // shared memory holds no more
     unsigned size = 1;
     while (size < MAXC && longest > 2048 * (int64_t)size &&
            (A.nseq * hkv * 2 * (int)size <= 2 * src->num_sms || longest > SEG * (int64_t)size))

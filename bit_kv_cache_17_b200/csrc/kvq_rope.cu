@@ -371,7 +371,9 @@ extern "C" int kvq_rope(const kvq_rope_params *p, const double *inv_freq, int64_
   A.half = half;
   A.adjacent = p->adjacent;
   A.sign = p->inverse ? -1.f : 1.f;
-  // a block takes the tokens whose units its threads hold at once; fewer tokens than blocks: one each
+  // a block takes the tokens whose units its threads hold at once (fewer tokens than blocks: one each) and
+  // stays for more: a thread reads its frequency once, six blocks an SM (16384 tokens of 48 heads, BF16:
+  // 70 us; eight blocks of four units a thread 74, a block for every group of tokens 78)
   const int64_t units = (n_q_heads && q_type == KVQ_DT_F32 ? 16ll : 8ll) * n_q_heads + 8ll * n_k_heads, held = UNITS * NT;
   A.tt = (int)std::max<int64_t>(1, std::min<int64_t>({held / units, n_tokens / (4 * 148), 32}));
   const unsigned grid = (unsigned)std::min<int64_t>((n_tokens + A.tt - 1) / A.tt, 148 * 6);
