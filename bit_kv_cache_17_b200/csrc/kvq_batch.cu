@@ -87,6 +87,8 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //    rescaled in tensor memory then), so most tiles need no correction and the two threads of a row
 //    only agree, by one barrier with an OR, that none is due.
 // Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
+// Calls of few rows (ONE), which memory or latency bounds, multiply the weights' remainders too; with
+// two tiles that costs 6 % and more (causal 8k prompt 613 us for 577).
 // Bound, many rows: the chain scores -> maximum -> exponentials -> weights of a tile against the other
 // group's products (causal 8k prompt of 40 heads, F16: 577 us, 1190 TFLOP/s; tensor pipe 53 %, exponentials
 // 48 %).  Bound, one row: HBM (65 536 tokens, 268 MB: 48 us + the join, 5.0 TB/s).
@@ -139,8 +141,8 @@ struct Ring {
   }
 };
 
-// LO: the keys have remainders (a rebuilt cache)
-template <bool F16, bool LO>
+// LO: the keys have remainders (a rebuilt cache).  ONE: no entry has more than one tile of query rows.
+template <bool F16, bool LO, bool ONE>
 __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
                                                 const __grid_constant__ CUtensorMap qmap,
                                                 const __grid_constant__ BArgs A) {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   const int sp = local % e.nsplit, head = local / e.nsplit % A.hkv;
   const int blk = e.nblk - 1 - local / e.nsplit / A.hkv;  // the last (causal: longest) first
   const int tok0 = blk * 2 * TB, tok1 = min(e.nq, tok0 + 2 * TB);
-  const bool halves = tok1 - tok0 <= TB;
+  const bool halves = ONE || tok1 - tok0 <= TB;
   const int ntile = halves ? 1 : 2;  // query tiles
   const int64_t lim_max = limit_of(A, e, tok1 - 1);
   const int kt = (int)((lim_max + BT - 1) / BT);
@@ -299,6 +301,12 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
             for (int s = 0; s < 4; ++s)
               tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 8 * s, v + (uint64_t)((4 * h + s) * (2048 >> 4)), idO,
                          h == 0 && s == 0 ? acc : 1u);
+            if (ONE) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 32 + 8 * s,
+                           v + (uint64_t)((4 * h + s) * (2048 >> 4)), idO, 1u);
+            }
           }
         }
       };
@@ -438,22 +446,44 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       const float sub = m == -INFINITY ? 0.f : -m;
       const tc::f2 sc = tc::pack2(A.qscale, A.qscale), ms = tc::pack2(sub, sub);
       tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
-      uint32_t w[32];
+      // P over the scores this thread has read; with ONE the weights' remainders behind it
+      if constexpr (ONE) {
 #pragma unroll
-      for (int v = 0; v < 32; ++v) {
-        float x0, x1;
-        const tc::f2 x = tc::fma2(tc::pack2(s[2 * v], s[2 * v + 1]), sc, ms);
-        if ((EMU >> (v & 7)) & 1) {
-          tc::ex2_fma<4>(x, x0, x1);
-        } else {
-          tc::unpack2(x, x0, x1);
-          x0 = tc::ex2(x0);
-          x1 = tc::ex2(x1);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[16], lo16[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            float x0, x1;
+            const int at = 32 * c + 2 * v;
+            tc::unpack2(tc::fma2(tc::pack2(s[at], s[at + 1]), sc, ms), x0, x1);
+            x0 = tc::ex2(x0);
+            x1 = tc::ex2(x1);
+            sum[v & 3] = tc::add2(sum[v & 3], tc::pack2(x0, x1));
+            hi[v] = tc::round2<F16>(x0, x1);
+            const float2 f = tc::widen2<F16>(hi[v]);
+            lo16[v] = tc::round2<F16>(x0 - f.x, x1 - f.y);
+          }
+          tc::tmem_st16(tS + 16 * c, hi);
+          tc::tmem_st16(tS + 32 + 16 * c, lo16);
         }
-        sum[v & 3] = tc::add2(sum[v & 3], tc::pack2(x0, x1));
-        w[v] = tc::round2<F16>(x0, x1);
+      } else {
+        uint32_t w[32];
+#pragma unroll
+        for (int v = 0; v < 32; ++v) {
+          float x0, x1;
+          const tc::f2 x = tc::fma2(tc::pack2(s[2 * v], s[2 * v + 1]), sc, ms);
+          if ((EMU >> (v & 7)) & 1) {
+            tc::ex2_fma<4>(x, x0, x1);
+          } else {
+            tc::unpack2(x, x0, x1);
+            x0 = tc::ex2(x0);
+            x1 = tc::ex2(x1);
+          }
+          sum[v & 3] = tc::add2(sum[v & 3], tc::pack2(x0, x1));
+          w[v] = tc::round2<F16>(x0, x1);
+        }
+        tc::tmem_st32(tS, w);
       }
-      tc::tmem_st32(tS, w);  // P over the scores this thread has read
       tc::tmem_wait_st();
       tc::fence_before();
       tc::mbar_arrive_warp(b_p + 8 * (2 * t + h));
@@ -471,7 +501,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       tc::fence_after();
     }
     // halves: group 1 leaves its own in the stages (all consumed), group 0 joins the two
-    const bool one = C.halves, join = one && tiles > 1, split = C.nsplit > 1;
+    const bool one = ONE || C.halves, join = one && tiles > 1, split = C.nsplit > 1;
     float *ex = reinterpret_cast<float *>(S + (one ? 1 : 2) * TILE);  // [128 rows][129], then m and l
     if (join && t == 1) {
 #pragma unroll 1
@@ -1150,8 +1180,8 @@ struct Plan {
 };
 
 // Blocks and key splits of up to MAXE entries: without splits when there is a block for every SM, or
-// no context is longer than four key tiles (one row over 512 tokens: 10.4 us either way, and one launch
-// less to issue); otherwise the fewest key tiles per CTA that one wave holds, down to one: the join, set
+// no context is longer than four key tiles (one row over 512 tokens: 12.4 us for about 10.4, but the
+// host issues one launch less, 4 to 5 us); otherwise the fewest key tiles per CTA that one wave holds, down to one: the join, set
 // up behind the attention, costs less than a tile (one row over 1024 / 2048 / 4096 tokens: 10.3 / 10.3 /
 // 12.4 us with splits of one tile and more, 13.1 / 13.9 / 14.3 us with at least four).
 void plan_attn(BEntry *e, int ne, int hkv, int G, int sms, int64_t *records) {
@@ -1400,11 +1430,11 @@ bool launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, cudaStre
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <bool F16, bool LO>
+template <bool F16, bool LO, bool ONE>
 int run_attn(const CUtensorMap &map, const CUtensorMap &qmap, const BArgs &A, unsigned ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(k_attn<F16, LO>, ATTN_SMEM, done)) return KVQ_E_CUDA;
-  k_attn<F16, LO><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
+  if (!allow_smem(k_attn<F16, LO, ONE>, ATTN_SMEM, done)) return KVQ_E_CUDA;
+  k_attn<F16, LO, ONE><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
   if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
   note_launches(1);
   return KVQ_OK;
@@ -1464,10 +1494,12 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   for (size_t base = 0; base < P.e.size(); base += MAXE) {
     const int ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
     int64_t ctas = 0, joins = 0;
+    bool one = true;
     A.ne = 0;
     for (int i = 0; i < ne; ++i) {
       BEntry e = P.e[base + i];
       if (e.nq == 0) continue;
+      one = one && e.nq <= BT / A.G;
       e.cta0 = (int)ctas;
       ctas += (int64_t)e.nblk * A.hkv * e.nsplit;
       if (e.nsplit > 1) joins += (int64_t)e.nq * n_q_heads;
@@ -1475,7 +1507,10 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
     }
     if (ctas == 0) continue;
     if (ctas > INT32_MAX) return KVQ_E_UNSUPPORTED;
-    const auto run = A.src.sides == 3 ? run_attn<true, true> : (A.src.f16 ? run_attn<true, false> : run_attn<false, false>);
+    const auto run = one ? (A.src.sides == 3 ? run_attn<true, true, true>
+                                             : (A.src.f16 ? run_attn<true, false, true> : run_attn<false, false, true>))
+                         : (A.src.sides == 3 ? run_attn<true, true, false>
+                                             : (A.src.f16 ? run_attn<true, false, false> : run_attn<false, false, false>));
     if (const int rc = run(map, qmap, A, (unsigned)ctas, st)) return rc;
     if (joins == 0) continue;
     if (joins > INT32_MAX) return KVQ_E_UNSUPPORTED;

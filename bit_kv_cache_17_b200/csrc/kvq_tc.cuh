@@ -265,5 +265,11 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
   return r;
 }
 
+// a pair of F16 or BF16 as fp32
+template <bool F16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  return ring2f(w, F16);
+}
+
 }  // namespace tc
 }  // namespace kvq
