@@ -87,8 +87,10 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //    rescaled in tensor memory then), so most tiles need no correction and the two threads of a row
 //    only agree, by one barrier with an OR, that none is due.
 // Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
-// Calls of few rows (ONE), which memory or latency bounds, multiply the weights' remainders too; with
-// two tiles that costs 6 % and more (causal 8k prompt 613 us for 577).
+// Calls of few rows (ONE) over up to ONE_TOKENS tokens, which latency bounds, multiply the weights'
+// remainders too and are as exact as their output's type; with two tiles that costs 6 % and more (causal
+// 8k prompt 613 us for 577), over long contexts power (one row over 65 536 tokens, many calls in a row:
+// 59.9 us for 56.0).
 // Bound, many rows: the chain scores -> maximum -> exponentials -> weights of a tile against the other
 // group's products (causal 8k prompt of 40 heads, F16: 577 us, 1190 TFLOP/s; tensor pipe 53 %, exponentials
 // 48 %).  Bound, one row: HBM (65 536 tokens, 268 MB: 48 us + the join, 5.0 TB/s).
@@ -101,6 +103,7 @@ constexpr int NT = 576;
 constexpr int TILE = BT * D * 2;   // bytes of a tile
 constexpr int HALF = TILE / 2;     // 64 channels of it
 constexpr int MAXST = 6;           // stages
+constexpr int ONE_TOKENS = 16384;
 constexpr float TAU = 8.f;         // lazy maximum, log2 units
 constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
 constexpr int MAXSPL = 64;
@@ -141,7 +144,8 @@ struct Ring {
   }
 };
 
-// LO: the keys have remainders (a rebuilt cache).  ONE: no entry has more than one tile of query rows.
+// LO: the keys have remainders (a rebuilt cache).  ONE: no entry has more than one tile of query rows, nor
+// more than ONE_TOKENS tokens.
 template <bool F16, bool LO, bool ONE>
 __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
                                                 const __grid_constant__ CUtensorMap qmap,
@@ -1499,7 +1503,7 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
     for (int i = 0; i < ne; ++i) {
       BEntry e = P.e[base + i];
       if (e.nq == 0) continue;
-      one = one && e.nq <= BT / A.G;
+      one = one && e.nq <= BT / A.G && e.n <= ONE_TOKENS;
       e.cta0 = (int)ctas;
       ctas += (int64_t)e.nblk * A.hkv * e.nsplit;
       if (e.nsplit > 1) joins += (int64_t)e.nq * n_q_heads;
