@@ -356,7 +356,7 @@ extern "C" int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int3
   if (src->p.n_kv_heads != dst->p.n_kv_heads) return KVQ_E_UNSUPPORTED;
   if (src->device != dst->device) return KVQ_E_INVAL;
   if (n_seqs == 0) return KVQ_OK;
-  if (!src_ids || !dst_ids || !mass || !workspace) return KVQ_E_INVAL;
+  if (!src_ids || !dst_ids || !mass) return KVQ_E_INVAL;
   if (mass_out && mass_out_ld < budget) return KVQ_E_INVAL;
   std::vector<char> seen(dst->p.n_seqs, 0);
   std::vector<EvictSeq> seqs;
@@ -378,9 +378,11 @@ extern "C" int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int3
       if (seen[src_ids[i]]) return KVQ_E_INVAL;
   if (mass_ld < most) return KVQ_E_INVAL;
   if (((uintptr_t)mass | (uintptr_t)kept | (uintptr_t)mass_out | (uintptr_t)workspace) & 15u) return KVQ_E_ALIGN;
+  // the indices go to `kept` where the caller wants them, else in front of the staged rows
   const bool staged = dst->fam_k != FAM_BF16;
-  size_t need;
-  if (const int rc = kvq_evict_workspace_bytes(src, dst, n_seqs, budget, &need)) return rc;
+  const size_t for_kept = kept ? 0 : kept_bytes(src, n_seqs, budget);
+  const size_t need = for_kept + (staged ? 2 * staged_bytes(src, (int64_t)n_seqs * budget) : 0);
+  if (need > 0 && !workspace) return KVQ_E_INVAL;
   if (ws_bytes < need) return KVQ_E_SIZE;
   if (const int rc = check_device(src)) return rc;
 
@@ -390,7 +392,7 @@ extern "C" int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int3
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   uint4 *stage_k = nullptr, *stage_v = nullptr;
   if (staged) {
-    stage_k = reinterpret_cast<uint4 *>(ws + kept_bytes(src, n_seqs, budget));
+    stage_k = reinterpret_cast<uint4 *>(ws + for_kept);
     stage_v = stage_k + staged_bytes(src, (int64_t)n_seqs * budget) / sizeof(uint4);
   }
   for (int base = 0; base < n_seqs; base += MAXE) {

@@ -620,14 +620,17 @@ class KVCache:
             out_ld = budget
         else:
             out_ld = self._mass_rows("evict", mass_out, n, "mass_out")
-        rc = _lib.kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget, self._size_ref)
-        if rc:
-            raise KVQError(rc, "kvq_evict_workspace_bytes")
-        nb = max(self._size.value, 16)
-        ws = mass.new_empty(nb, dtype=torch.uint8)
+        ptr = nb = 0
+        if dst.params.type_k != 0:
+            rc = _lib.kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget, self._size_ref)
+            if rc:
+                raise KVQError(rc, "kvq_evict_workspace_bytes")
+            nb = self._size.value
+            ws = mass.new_empty(nb, dtype=torch.uint8)
+            ptr = ws.data_ptr()
         rc = _lib.kvq_evict(self.handle, layer, dst.handle, dst_layer, n, _i32arr(seq_ids), _i32arr(dst_ids),
                             mass.data_ptr(), ld, budget, sink, recent, kept.data_ptr(), mass_out.data_ptr(), out_ld,
-                            ws.data_ptr(), nb, self._raw_stream(self._index))
+                            ptr, nb, self._raw_stream(self._index))
         if rc:
             raise KVQError(rc, "kvq_evict")
         return kept, mass_out

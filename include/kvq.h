@@ -347,7 +347,8 @@ int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *se
                   float decay, const float *mass_in, float *mass_out, int64_t mass_ld, void *workspace,
                   size_t ws_bytes, kvq_stream_t stream);
 
-/* Workspace bytes kvq_evict needs: the kept indices, and for a quantized destination the kept rows. */
+/* Workspace bytes kvq_evict needs at most: the kept indices (not where the call gets `kept`), and for a
+ * quantized destination the kept rows. */
 int kvq_evict_workspace_bytes(const kvq_cache *src, const kvq_cache *dst, int32_t n_seqs, int32_t budget,
                               size_t *bytes);
 

@@ -153,6 +153,30 @@ def test_streams_and_graph():
     assert t.equal(want[0], got[0]) and t.equal(want[1], got[1]) and t.equal(a.rows16(0), c.rows16(0))
 
 
+def test_indices_in_the_workspace():
+    """Without `kept` and `mass_out` the indices live in the workspace, which then has to be there."""
+    t = P.torch()
+    k, v = P.kv(17, [300], 2)
+    src = P.cache("bf16", [300], 2, k, v)
+    st = t.cuda.current_stream().cuda_stream
+    w = t.rand(1, 2, 300, device="cuda")
+    for type_ in ("bf16", "q8_0"):
+        a, b = (kvq.KVCache(n_kv_heads=2, max_ctx=120, type_k=type_, type_v=type_, tail=16) for _ in range(2))
+        src.evict(a, 0, 0, [0], [0], w, 120, recent=20)
+        need = kvq.kvq_evict_workspace_bytes(src.handle, b.handle, 1, 120)
+        ws = t.empty(need, dtype=t.uint8, device="cuda")
+        args = (src.handle, 0, b.handle, 0, [0], [0], w.data_ptr(), 300, 120, 0, 20, 0, 0, 0)
+        with pytest.raises(kvq.KVQError) as e:
+            kvq.kvq_evict(*args, 0, need, st)
+        assert e.value.code == kvq.KVQ_E_INVAL
+        with pytest.raises(kvq.KVQError) as e:
+            kvq.kvq_evict(*args, ws.data_ptr(), need - 1, st)
+        assert e.value.code == kvq.KVQ_E_SIZE
+        kvq.kvq_evict(*args, ws.data_ptr(), need, st)
+        for which in (0, 1):
+            assert t.equal(a.dequant(0, 0, which, 0, 120), b.dequant(0, 0, which, 0, 120))
+
+
 def test_refusals_change_nothing():
     t = P.torch()
     k, v = P.kv(15, [100, 30], 2)
