@@ -347,7 +347,7 @@ extern "C" int kvq_rope(const kvq_rope_params *p, const double *inv_freq, int64_
     return KVQ_E_UNSUPPORTED;
   if (n_tokens > INT32_MAX || n_q_heads > 65536 || n_k_heads > 65536) return KVQ_E_INVAL;
   if (n_tokens == 0 || n_q_heads + n_k_heads == 0) return KVQ_OK;
-  if (!pos || pos_ld < n_tokens || pos_ld > INT64_MAX / 32) return KVQ_E_INVAL;
+  if (!pos || (pos_ld != 0 && pos_ld < n_tokens) || pos_ld > INT64_MAX / 32) return KVQ_E_INVAL;
   if ((uintptr_t)pos & 3u) return KVQ_E_ALIGN;
   int rc = check_rows(n_tokens, n_q_heads, q, q_type, q_ld, q_out, q_out_type, q_out_ld);
   if (rc == KVQ_OK) rc = check_rows(n_tokens, n_k_heads, k, KVQ_DT_BF16, k_ld, k_out, KVQ_DT_BF16, k_out_ld);

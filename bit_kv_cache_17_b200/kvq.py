@@ -332,7 +332,8 @@ class Rope:
         return s[1], x.data_ptr(), st[0] if n > 1 else max(st[0], s[1] * 128)
 
     def apply(self, pos, q=None, k=None, q_dtype=None, inverse=False, q_out=None, k_out=None, stream=None):
-        """pos: int32 [n_axes, tokens] (or [tokens] for one axis); q: [tokens, heads, 128] fp32, BF16
+        """pos: int32 [n_axes, tokens] (or [tokens] for one axis; one row expanded over the axes is
+        read as it is); q: [tokens, heads, 128] fp32, BF16
         or F16, a slice of a packed row allowed; k: BF16 likewise.  Returns (q_out, k_out), new
         contiguous tensors (q of q_dtype, its own type by default) unless given; an output may be its
         input."""
@@ -349,7 +350,7 @@ class Rope:
         n = shape[1]
         if pos.dtype is not torch.int32 or len(shape) != 2 or shape[0] != self.n_axes or (n > 1 and pos.stride(1) != 1):
             _refuse("Rope.apply", "pos is int32 [n_axes, tokens], the tokens contiguous")
-        pos_ld = max(pos.stride(0), n) if self.n_axes > 1 else n
+        pos_ld = pos.stride(0) if self.n_axes > 1 else n  # (0: a row expanded over the axes)
         a, b = (0, 0, 0, 0, 0, 0, 0), (0, 0, 0, 0, 0)
         if q is not None:
             h, ptr, ld = self._rows(q, n, dev, "q")

@@ -296,7 +296,7 @@ void kvq_rope_default_params(kvq_rope_params *p);
  * the attention calls, which take rotated rows.
  * inv_freq: host, rot_dim / 2 frequencies f_i in place of theta's (any scaling of the base), or NULL.
  * pos: device int32, pos[a * pos_ld + t] the position of token t on axis a (any value; the angle is
- * reduced in 64 bits).  q: device rows [n_tokens][n_q_heads][128] of q_type, token t at element
+ * reduced in 64 bits); pos_ld is 0 (one row for all axes, text tokens) or >= n_tokens.  q: device rows [n_tokens][n_q_heads][128] of q_type, token t at element
  * t * q_ld (a slice of a packed q|k|v row is a q_ld larger than n_q_heads * 128); q_out likewise, of
  * q_out_type.  k, k_out: BF16 rows, as kvq_append takes them.  n_q_heads or n_k_heads may be 0 (its
  * pointers are then not looked at).  An output may be its own input (same type and ld); otherwise

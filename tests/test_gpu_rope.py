@@ -121,6 +121,19 @@ def test_only_q_only_k_and_no_tokens():
     assert t.equal(a1, a[1:2])
 
 
+@pytest.mark.parametrize("n", [1, 300])
+def test_one_row_of_positions_for_all_axes(n):
+    t = P.torch()
+    r = kvq.Rope((16, 24, 24), turns=True)
+    x = t.randn(n, 3, 128, generator=t.Generator().manual_seed(n)).bfloat16().cuda()
+    row = positions(n, 1, n, 5000)[0].cuda()
+    want, _ = r.apply(row.repeat(3, 1), q=x)
+    assert t.equal(r.apply(row.expand(3, n), q=x)[0], want)
+    if n > 2:  # rows that overlap
+        with pytest.raises(kvq.KVQError):
+            r.apply(row.as_strided((3, n - 2), (1, 1)), q=x[:n - 2])
+
+
 def test_inverse_is_the_gradient():
     """The gradient of sum(w . rope(x)) by x is rope_inverse(w): against differences of the fp32 result."""
     t = P.torch()

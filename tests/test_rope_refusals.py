@@ -67,6 +67,29 @@ def test_binding_refuses():
             r.apply(bad, q=t.zeros(3, 1, 128))
 
 
+@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("expanded", [False, True])
+def test_the_stride_of_the_positions_is_passed_as_it_is(monkeypatch, n, expanded):
+    """One row expanded over the axes has stride 0: any other number would be read past its end."""
+    import types
+
+    import torch as t
+
+    class OnDevice(t.Tensor):
+        def get_device(self):
+            return 0
+
+    rope, calls = kvq.Rope((16, 24, 24)), []
+    rope.torch = types.SimpleNamespace(cuda=types.SimpleNamespace(current_device=lambda: 0), int32=t.int32,
+                                       empty_like=t.empty_like, contiguous_format=t.contiguous_format)
+    rope._raw_stream = lambda index: 0
+    monkeypatch.setattr(kvq, "_lib", types.SimpleNamespace(kvq_rope=lambda *a: calls.append(a) or 0))
+    row = t.arange(n, dtype=t.int32)
+    pos = (row.expand(3, n) if expanded else row.repeat(3, 1)).as_subclass(OnDevice)
+    rope.apply(pos, q=t.zeros(n, 2, 128).as_subclass(OnDevice))
+    assert calls[0][3] == pos.data_ptr() and calls[0][4] == (0 if expanded else n)
+
+
 def test_null_handles_are_refused():
     L = kvq._lib
     n = C.c_size_t()
