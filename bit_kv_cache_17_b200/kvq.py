@@ -404,9 +404,7 @@ class KVCache:
         self._index = self.storage.get_device()
         self._t16 = torch.float16 if self.params.tail_f16 else torch.bfloat16
         self._raw_stream = _raw_stream_of(torch)
-        self._size = _sz()
         self._rows16 = {}  # layer -> view
-        self._size_ref = C.byref(self._size)
         self._ws = None
         self._ws_bytes = {}  # (n_seqs, n_q_heads) -> kvq_workspace_bytes
 
@@ -518,10 +516,11 @@ class KVCache:
 
     def _batch_workspace(self, layer, n, ids, nq, hq):
         """(the tensor that owns it or None, pointer, bytes)"""
-        rc = _lib.kvq_batch_workspace_bytes(self.handle, layer, n, ids, nq, hq, self._size_ref)
+        size = _sz()  # of this call: the library runs without the interpreter's lock
+        rc = _lib.kvq_batch_workspace_bytes(self.handle, layer, n, ids, nq, hq, C.byref(size))
         if rc:
             raise KVQError(rc, "kvq_batch_workspace_bytes")
-        nb = self._size.value
+        nb = size.value
         if nb == 0:
             return None, 0, 0
         ws = self.torch.empty(nb, dtype=self.torch.uint8, device=self.storage.device)
@@ -623,10 +622,11 @@ class KVCache:
             out_ld = self._mass_rows("evict", mass_out, n, "mass_out")
         ptr = nb = 0
         if dst.params.type_k != 0:
-            rc = _lib.kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget, self._size_ref)
+            size = _sz()
+            rc = _lib.kvq_evict_workspace_bytes(self.handle, dst.handle, n, budget, C.byref(size))
             if rc:
                 raise KVQError(rc, "kvq_evict_workspace_bytes")
-            nb = self._size.value
+            nb = size.value
             ws = mass.new_empty(nb, dtype=torch.uint8)
             ptr = ws.data_ptr()
         rc = _lib.kvq_evict(self.handle, layer, dst.handle, dst_layer, n, _i32arr(seq_ids), _i32arr(dst_ids),
