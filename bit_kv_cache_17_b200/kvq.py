@@ -278,6 +278,8 @@ class _On:
     each have their own."""
 
     def __init__(self, torch, device, stream):
+        if stream is not None and stream.device != device:
+            _refuse("stream", f"a stream of {stream.device} for tensors on {device}")
         self.both = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):

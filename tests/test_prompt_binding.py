@@ -33,3 +33,12 @@ def test_calls_that_overlap_size_their_own_workspaces(monkeypatch):
     monkeypatch.setattr(kvq, "_lib", types.SimpleNamespace(kvq_batch_workspace_bytes=workspace_bytes))
     ws, ptr, nb = c._batch_workspace(0, 1, None, None, 8)
     assert nb == 128 and ws.numel() == 128 and ptr == ws.data_ptr()
+
+
+def test_a_stream_of_another_device_is_refused():
+    import torch as t
+
+    stream = types.SimpleNamespace(device=t.device("cuda", 1))
+    with pytest.raises(kvq.KVQError):
+        kvq._On(t, t.device("cuda", 0), stream)
+    assert len(kvq._On(t, t.device("cuda", 1), None).both) == 1
