@@ -1477,6 +1477,8 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   if (P.rows == 0) return KVQ_OK;
   if (!q || !out || (!workspace && P.bytes > 0)) return KVQ_E_INVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return KVQ_E_ALIGN;
+  const uint64_t row_bytes = (uint64_t)P.rows * n_q_heads * D * 2;
+  if (overlap(q, row_bytes, out, row_bytes)) return KVQ_E_INVAL;
   if (ws_bytes < P.bytes) return KVQ_E_SIZE;
   if (const int rc = check_device(c)) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -1539,7 +1541,10 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   if (most == 0) return KVQ_OK;
   if (!mass_out || (decay != 0.f && !mass_in) || (P.rows > 0 && (!q || !lse)) || (!workspace && P.bytes > 0))
     return KVQ_E_INVAL;
-  if (mass_ld < most) return KVQ_E_INVAL;
+  const int64_t mass_rows = (int64_t)n_seqs * c->p.n_kv_heads;
+  if (mass_ld < most || mass_ld > INT64_MAX / 8 / mass_rows) return KVQ_E_INVAL;
+  const uint64_t mass_bytes = (uint64_t)(mass_rows * mass_ld) * sizeof(float);
+  if (decay != 0.f && mass_in != mass_out && overlap(mass_in, mass_bytes, mass_out, mass_bytes)) return KVQ_E_INVAL;
   if (!aligned16(q) || !aligned16(lse) || !aligned16(mass_in) || !aligned16(mass_out) || !aligned16(workspace))
     return KVQ_E_ALIGN;
   if (ws_bytes < P.bytes) return KVQ_E_SIZE;

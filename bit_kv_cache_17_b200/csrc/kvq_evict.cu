@@ -376,7 +376,13 @@ extern "C" int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int3
   if (src == dst && src_layer == dst_layer)
     for (int i = 0; i < n_seqs; ++i)
       if (seen[src_ids[i]]) return KVQ_E_INVAL;
-  if (mass_ld < most) return KVQ_E_INVAL;
+  const int64_t head_rows = (int64_t)n_seqs * src->p.n_kv_heads, most_ld = INT64_MAX / 8 / head_rows;
+  if (mass_ld < most || mass_ld > most_ld || (mass_out && mass_out_ld > most_ld)) return KVQ_E_INVAL;
+  const auto bytes = [&](int64_t ld) { return (uint64_t)(head_rows * ld) * sizeof(float); };
+  if (overlap(mass, bytes(mass_ld), kept, bytes(budget)) ||
+      overlap(mass, bytes(mass_ld), mass_out, bytes(mass_out_ld)) ||
+      overlap(kept, bytes(budget), mass_out, bytes(mass_out_ld)))
+    return KVQ_E_INVAL;
   if (((uintptr_t)mass | (uintptr_t)kept | (uintptr_t)mass_out | (uintptr_t)workspace) & 15u) return KVQ_E_ALIGN;
   // the indices go to `kept` where the caller wants them, else in front of the staged rows
   const bool staged = dst->fam_k != FAM_BF16;

@@ -55,6 +55,12 @@ inline int64_t keep_start(const kvq_cache *c, int fam, int64_t n) {
   return fam == FAM_KVARN ? (Q / GROUP) * GROUP : Q;
 }
 
+// Whether na bytes at a and nb bytes at b (either may be NULL) share any.
+inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x && y && na && nb && (x < y ? y - x < na : x - y < nb);
+}
+
 LayerView layer_view(const kvq_cache *c, int layer);
 
 struct AppendSeq {

@@ -296,9 +296,9 @@ void kvq_rope_default_params(kvq_rope_params *p);
  * the attention calls, which take rotated rows.
  * inv_freq: host, rot_dim / 2 frequencies f_i in place of theta's (any scaling of the base), or NULL.
  * pos: device int32, pos[a * pos_ld + t] the position of token t on axis a (any value; the angle is
- * reduced in 64 bits); pos_ld is 0 (one row for all axes, text tokens) or >= n_tokens.  q: device rows [n_tokens][n_q_heads][128] of q_type, token t at element
- * t * q_ld (a slice of a packed q|k|v row is a q_ld larger than n_q_heads * 128); q_out likewise, of
- * q_out_type.  k, k_out: BF16 rows, as kvq_append takes them.  n_q_heads or n_k_heads may be 0 (its
+ * reduced in 64 bits); pos_ld is 0 (one row for all axes, text tokens) or >= n_tokens.
+ * q: device rows [n_tokens][n_q_heads][128] of q_type, token t at element t * q_ld (a slice of a
+ * packed q|k|v row is a q_ld larger than n_q_heads * 128); q_out likewise, of q_out_type.  k, k_out: BF16 rows, as kvq_append takes them.  n_q_heads or n_k_heads may be 0 (its
  * pointers are then not looked at).  An output may be its own input (same type and ld); otherwise
  * the spans from the first to the last row of the two must not overlap (KVQ_E_INVAL).  Pointers and
  * row strides are multiples of 16 bytes (KVQ_E_ALIGN; pos: 4).  Arithmetic is fp32 with one rounding
@@ -319,8 +319,8 @@ int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs,
  * tokens, n_q[e] <= n).  Entry e is n_q[e] >= 0 query tokens over sequence seq_ids[e]; a sequence may
  * be listed several times (beams over one encoder state).
  * q: device [sum(n_q), n_q_heads, 128] in the cache's 16-bit format (BF16, or F16 with tail_f16),
- * the rows of entry 0 first; out: same shape and type; lse: device fp32 [sum(n_q), n_q_heads] or
- * NULL: log of the sum of exp(scale q.k) of each row.  softmax_scale <= 0 selects 1/sqrt(128).
+ * the rows of entry 0 first; out: same shape and type, sharing no byte with q (KVQ_E_INVAL); lse:
+ * device fp32 [sum(n_q), n_q_heads] or NULL: log of the sum of exp(scale q.k) of each row.  softmax_scale <= 0 selects 1/sqrt(128).
  * A row that sees no token gives zeros and lse = -inf.  Cached values must be finite (a value that is
  * not reaches every row that attends to its 128-token tile, also where the row does not see it).
  * workspace: device, >= kvq_batch_workspace_bytes (NULL where that is 0); calls that may overlap on
@@ -339,9 +339,9 @@ int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *s
  * mass_out[e][h][t] = decay * mass_in[e][h][t] + sum over the rows of entry e and the query heads
  * of KV head h that see token t of exp(scale q.k - lse), for t < n; places behind the sequence's
  * last token are left as they were.  mass_in, mass_out: device fp32, [n_seqs][n_kv_heads][mass_ld],
- * mass_ld >= the longest listed sequence; mass_out may be mass_in; decay in [0, 1], and with decay 0
- * mass_in is not read (NULL allowed).  lse: as kvq_batch_attn (or any call over the same rows)
- * wrote it; rows with lse = -inf weigh nothing.  The other arguments are kvq_batch_attn's. */
+ * mass_ld >= the longest listed sequence; mass_out may be mass_in, and may not overlap it otherwise
+ * (KVQ_E_INVAL); decay in [0, 1], and with decay 0 mass_in is not read (NULL allowed).  lse: as
+ * kvq_batch_attn (or any call over the same rows) wrote it; rows with lse = -inf weigh nothing.  The other arguments are kvq_batch_attn's. */
 int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids, const int32_t *n_q,
                   int32_t n_q_heads, int32_t causal, const void *q, float softmax_scale, const float *lse,
                   float decay, const float *mass_in, float *mass_out, int64_t mass_ld, void *workspace,
@@ -363,8 +363,9 @@ int kvq_evict_workspace_bytes(const kvq_cache *src, const kvq_cache *dst, int32_
  * mass: device fp32 [n_seqs][n_kv_heads][mass_ld], mass_ld >= every n.  kept: device int32
  * [n_seqs][n_kv_heads][budget] or NULL: the kept tokens' old indices in ascending order, -1 behind
  * them.  mass_out: device fp32 [n_seqs][n_kv_heads][mass_out_ld >= budget] or NULL: the kept
- * tokens' weights, zeros behind them.  Neither may overlap mass.  dst_ids are distinct; with dst ==
- * src and the same layer none of them may be among src_ids (KVQ_E_INVAL).  sink + recent <= budget.
+ * tokens' weights, zeros behind them.  None of the three may overlap another (KVQ_E_INVAL).
+ * dst_ids are distinct; with dst == src and the same layer none of them may be among src_ids
+ * (KVQ_E_INVAL).  sink + recent <= budget.
  * Keys keep the rotation they were appended with; positions of later tokens are the caller's
  * (kvq_rope takes them explicitly). */
 int kvq_evict(kvq_cache *src, int32_t src_layer, kvq_cache *dst, int32_t dst_layer, int32_t n_seqs,

@@ -154,3 +154,20 @@ def test_refusals():
     assert code(0, [0], [8], q, lse, mass_in=m.double()) == kvq.KVQ_E_INVAL
     assert code(0, [0], [8], q, lse, mass_in=m.expand(1, 2, 100)[:, :1]) == kvq.KVQ_E_INVAL
     assert code(0, [0], [101], q, lse, causal=True) == kvq.KVQ_E_INVAL
+
+
+def test_weights_that_overlap_without_being_one_are_refused():
+    t = P.torch()
+    k, v = P.kv(3, [100], 2)
+    c = P.cache("bf16", [100], 2, k, v)
+    q = P.queries(3, 8, 4, t.bfloat16)
+    lse = t.zeros(8, 4, device="cuda")
+    m = t.zeros(3, 2, 100, device="cuda").view(-1)
+    at = lambda i: m[i:i + 200].view(1, 2, 100)  # noqa: E731
+    for a, b in ((0, 100), (100, 0), (0, 196)):
+        with pytest.raises(kvq.KVQError) as e:
+            c.attn_mass(0, [0], [8], q, lse, mass_in=at(a), mass_out=at(b))
+        assert e.value.code == kvq.KVQ_E_INVAL
+    assert not m.any()
+    c.attn_mass(0, [0], [8], q, lse, mass_in=at(0), mass_out=at(200))
+    c.attn_mass(0, [0], [8], q, lse, decay=0.0, mass_in=at(0), mass_out=at(100))  # not read

@@ -178,3 +178,18 @@ def test_refusals():
                 st) == kvq.KVQ_E_ALIGN
     assert code(kvq.kvq_batch_attn, *args, 2, q.data_ptr(), 0.0, out.data_ptr(), 0, ws.data_ptr(), need,
                 st) == kvq.KVQ_E_INVAL
+
+
+def test_an_output_over_its_queries_is_refused():
+    t = P.torch()
+    k, v = P.kv(3, [100], 2)
+    c = P.cache("bf16", [100], 2, k, v)
+    both = t.zeros(120, 4, 128, dtype=t.bfloat16, device="cuda")
+    n0 = kvq.kvq_launch_count()
+    for a, b in ((0, 0), (0, 59), (59, 0)):
+        with pytest.raises(kvq.KVQError) as e:
+            c.batch_attn(0, [0], [60], both[a:a + 60], out=both[b:b + 60])
+        assert e.value.code == kvq.KVQ_E_INVAL
+    assert kvq.kvq_launch_count() == n0
+    c.batch_attn(0, [0], [60], both[:60], out=both[60:])  # neighbours
+    assert kvq.kvq_launch_count() > n0

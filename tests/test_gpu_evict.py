@@ -208,3 +208,21 @@ def test_refusals_change_nothing():
     q = P.cache("q8_0", [100, 30], 2, k, v)
     assert code(q.evict, dst, 0, 0, [0], [0], w[:1], 40) == kvq.KVQ_E_UNSUPPORTED
     assert dst.seq_len(0, 0) == 0 and dst.seq_len(0, 1) == 0 and src.seq_len(0, 0) == 100
+
+
+def test_outputs_over_the_weights_are_refused():
+    t = P.torch()
+    k, v = P.kv(15, [100], 2)
+    src = P.cache("bf16", [100], 2, k, v)
+    dst = kvq.KVCache(n_seqs=1, n_kv_heads=2, max_ctx=50, type_k="bf16", type_v="bf16", tail=0)
+    w = t.rand(1, 2, 100, device="cuda")
+    before = w.clone()
+    part = w.view(-1)[40:120].view(1, 2, 40)
+    rows = t.zeros(1, 2, 40, dtype=t.int32, device="cuda")
+    n0 = kvq.kvq_launch_count()
+    for kw in (dict(mass_out=part), dict(kept=part.view(t.int32)), dict(kept=rows, mass_out=rows.view(t.float32)),
+               dict(mass_out=w)):
+        with pytest.raises(kvq.KVQError) as e:
+            src.evict(dst, 0, 0, [0], [0], w, 40, **kw)
+        assert e.value.code == kvq.KVQ_E_INVAL
+    assert kvq.kvq_launch_count() == n0 and t.equal(w, before) and dst.seq_len(0, 0) == 0
