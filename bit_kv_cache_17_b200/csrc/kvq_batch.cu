@@ -1012,23 +1012,22 @@ __global__ void __launch_bounds__(256) k_mass_join(const __grid_constant__ BArgs
   A.mass_out[at] = A.decay != 0.f ? A.decay * A.mass_in[at] + v : v;
 }
 
-// BF16 queries as F16 rows, for the products with a rebuilt cache (exact in the F16 range)
-__global__ void __launch_bounds__(256) k_q16(const uint4 *q, uint4 *dst, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) dst[i] = bf16x8_to_ring(q[i], 1);
-}
-
 // ---- quantized caches: values rebuilt in the original basis as F16 rows --------------------------
 // A warp takes four tokens of a (slot, head, side); a token belongs to eight lanes, 16 channels each
 // (lane part p: channels 4 p + 32 j + (0..3), j = 0..3: one 32-bit word of the stored planes per
 // block).  Keys are kept as an F16 high part and the F16 remainder (22 bits: a score is an exponent, and
 // the log-sum-exp and the weights are fp32 results); values, whose result is rounded to 16 bits, as one F16.  Bound: the stores
 // (9.2 k tokens of 8 heads, q8_0, K and V in one launch: 18 us for 72 MB written, 20 MB read).
+// The blocks behind the slots' turn BF16 queries into F16 rows for the products (exact in the F16 range).
 constexpr int MAXR = 128;  // slots per launch
 struct Rebuild {
   int32_t n, which;  // slots; side (2: K and V, by blockIdx.y)
   int64_t cap;
   int32_t first;     // slot of entry 0
+  int32_t blocks;    // those of the slots
+  const uint4 *q;    // BF16 queries to convert, nq pieces of 8, or none
+  uint4 *q16;
+  int64_t nq;
   struct {
     int32_t seq, n, Q, block0;
   } s[MAXR];
@@ -1039,6 +1038,11 @@ template <int FAM, int BITS>
 __global__ void __launch_bounds__(256) k_rebuild(LayerView L, const __grid_constant__ Rebuild R, uint16_t *dst) {
   constexpr int WL = plane_lo(BITS), WH = plane_hi(BITS);
   const int lane = threadIdx.x & 31, part = lane & 7;
+  if ((int)blockIdx.x >= R.blocks) {
+    const int64_t at = (int64_t)((int)blockIdx.x - R.blocks) * 256 + threadIdx.x;
+    if (blockIdx.y == 0 && at < R.nq) R.q16[at] = bf16x8_to_ring(R.q[at], 1);
+    return;
+  }
   int i = 0;
   while (i + 1 < R.n && R.s[i + 1].block0 <= (int)blockIdx.x) ++i;
   const int per = (R.s[i].n + RT - 1) / RT, local = blockIdx.x - R.s[i].block0;
@@ -1308,9 +1312,16 @@ int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids,
   return KVQ_OK;
 }
 
+// Where a call's F16 queries go.
+uint4 *q16_rows(const Plan &P, void *workspace) {
+  return reinterpret_cast<uint4 *>(static_cast<uint8_t *>(workspace) + P.rebuilt_bytes + P.part_bytes);
+}
+
 // Rebuilds what a quantized cache needs and names the source of the rows.
-int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, void *workspace, cudaStream_t st,
-                Source *s) {
+// Queries to convert go along with the first launch (a launch of their own costs the host 4 us); without a
+// sequence to rebuild nothing reads them.
+int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, const void *q, int n_q_heads,
+                void *workspace, cudaStream_t st, Source *s) {
   const LayerView L = layer_view(c, layer);
   if (c->fam_k == FAM_BF16) {
     *s = Source{reinterpret_cast<const uint16_t *>(L.ring), L.ring_cap, c->p.n_seqs, L.tail_f16, 2};
@@ -1319,7 +1330,7 @@ int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, void 
   uint16_t *dst = static_cast<uint16_t *>(workspace);
   *s = Source{dst, std::max<int64_t>(P.cap, 1), std::max(1, (int)P.slot_seq.size()), 1, 3};
   for (size_t base = 0; base < P.slot_seq.size(); base += MAXR) {
-    Rebuild R;
+    Rebuild R{};
     R.n = (int)std::min<size_t>(MAXR, P.slot_seq.size() - base);
     R.cap = P.cap;
     R.first = (int)base;
@@ -1331,13 +1342,22 @@ int make_source(const kvq_cache *c, int layer, const Plan &P, bool values, void 
       blocks += (n + RT - 1) / RT * c->p.n_kv_heads;
       if (blocks > INT32_MAX) return KVQ_E_UNSUPPORTED;
     }
+    R.blocks = (int32_t)blocks;
+    if (base == 0 && P.q16_bytes) {
+      R.q = static_cast<const uint4 *>(q);
+      R.q16 = q16_rows(P, workspace);
+      R.nq = P.rows * n_q_heads * (D / 8);
+    }
     const bool both = values && c->p.type_k == c->p.type_v;
     for (int which = 0; which < (values && !both ? 2 : 1); ++which) {
       R.which = both ? 2 : which;
-      if (rebuild(which ? c->fam_v : c->fam_k, which ? c->bits_v : c->bits_k, L, R, (unsigned)blocks, dst, st) !=
+      const int64_t grid = blocks + (R.nq + 255) / 256;
+      if (grid > INT32_MAX) return KVQ_E_UNSUPPORTED;
+      if (rebuild(which ? c->fam_v : c->fam_k, which ? c->bits_v : c->bits_k, L, R, (unsigned)grid, dst, st) !=
           cudaSuccess)
         return KVQ_E_CUDA;
       note_launches(1);
+      R.nq = 0;
     }
   }
   return KVQ_OK;
@@ -1391,18 +1411,9 @@ int map_queries(const void *q, int f16, int hkv, int G, int64_t rows, CUtensorMa
              : KVQ_E_CUDA;
 }
 
-// The query rows as the kernels read them: converted first where a BF16 tail meets F16 products.
-int make_queries(const Plan &P, const void *q, int f16, int hkv, int n_q_heads, void *workspace, cudaStream_t st,
-                 CUtensorMap *map) {
-  if (P.q16_bytes) {
-    uint4 *q16 = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(workspace) + P.rebuilt_bytes + P.part_bytes);
-    const int64_t n = P.rows * n_q_heads * (D / 8);
-    k_q16<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(static_cast<const uint4 *>(q), q16, n);
-    if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
-    note_launches(1);
-    q = q16;
-  }
-  return map_queries(q, f16, hkv, n_q_heads / hkv, P.rows, map);
+// The query rows as the kernels read them: the converted ones where a BF16 tail meets F16 products.
+int make_queries(const Plan &P, const void *q, int f16, int hkv, int n_q_heads, void *workspace, CUtensorMap *map) {
+  return map_queries(P.q16_bytes ? q16_rows(P, workspace) : q, f16, hkv, n_q_heads / hkv, P.rows, map);
 }
 
 // The dynamic shared memory of a kernel, allowed once per device.
@@ -1483,10 +1494,10 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   if (const int rc = check_device(c)) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BArgs A{};
-  if (const int rc = make_source(c, layer, P, true, workspace, st, &A.src)) return rc;
+  if (const int rc = make_source(c, layer, P, true, q, n_q_heads, workspace, st, &A.src)) return rc;
   CUtensorMap map, qmap;
   if (const int rc = map_rows(A.src, c->p.n_kv_heads, &map)) return rc;
-  if (const int rc = make_queries(P, q, A.src.f16, c->p.n_kv_heads, n_q_heads, workspace, st, &qmap)) return rc;
+  if (const int rc = make_queries(P, q, A.src.f16, c->p.n_kv_heads, n_q_heads, workspace, &qmap)) return rc;
   A.hkv = c->p.n_kv_heads;
   A.G = n_q_heads / c->p.n_kv_heads;
   A.causal = causal;
@@ -1551,7 +1562,7 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   if (const int rc = check_device(c)) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BArgs A{};
-  if (const int rc = make_source(c, layer, P, false, workspace, st, &A.src)) return rc;
+  if (const int rc = make_source(c, layer, P, false, q, n_q_heads, workspace, st, &A.src)) return rc;
   A.hkv = c->p.n_kv_heads;
   A.G = n_q_heads / c->p.n_kv_heads;
   A.causal = causal;
@@ -1568,7 +1579,7 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   CUtensorMap kmap, qmap{};
   if (const int rc = map_rows(A.src, A.hkv, &kmap)) return rc;
   if (P.rows > 0)
-    if (const int rc = make_queries(P, q, A.src.f16, A.hkv, n_q_heads, workspace, st, &qmap)) return rc;
+    if (const int rc = make_queries(P, q, A.src.f16, A.hkv, n_q_heads, workspace, &qmap)) return rc;
   for (size_t base = 0; base < P.e.size(); base += MAXE) {
     const int ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
     int64_t ctas = 0, joins = 0;
