@@ -193,3 +193,31 @@ def test_an_output_over_its_queries_is_refused():
     assert kvq.kvq_launch_count() == n0
     c.batch_attn(0, [0], [60], both[:60], out=both[60:])  # neighbours
     assert kvq.kvq_launch_count() > n0
+
+
+@pytest.mark.parametrize("m", [3, 200])
+def test_rebuilt_calls_one_after_another_and_in_a_graph(m):
+    """The attention is set up behind the launch that rebuilds the cache and converts the queries:
+    calls in a row, which take the same workspace, and replays give what single calls give."""
+    t = P.torch()
+    lens = [700, 0, 3000]
+    k, v = P.kv(8, lens, 2)
+    c = P.cache("q8_0", lens, 2, k, v, tail=128)
+    n_q = [m, 2, m]
+    qs = [P.queries(40 + i, sum(n_q), 10, t.bfloat16) for i in range(8)]
+    want = []
+    for q in qs:
+        want.append(c.batch_attn(0, [0, 1, 2], n_q, q, return_lse=True))
+        t.cuda.synchronize()
+    for _ in range(3):
+        got = [c.batch_attn(0, [0, 1, 2], n_q, q, return_lse=True) for q in qs]
+        for (a, la), (b, lb) in zip(want, got):
+            assert t.equal(a, b) and t.equal(la, lb)
+    q = qs[0].clone()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        out, lse = c.batch_attn(0, [0, 1, 2], n_q, q, return_lse=True)
+    for x, (a, la) in zip(qs, want):
+        q.copy_(x)
+        g.replay()
+        assert t.equal(out, a) and t.equal(lse, la)
