@@ -109,8 +109,8 @@ constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, ac
 constexpr int MAXSPL = 64;
 constexpr int EXG = BT * 129 + 2 * BT;  // floats a group leaves in the stages at the end (rows padded to 129)
 static_assert(2 * EXG * 4 <= 5 * TILE, "two groups' rows fit the stages");
-// which of eight score pairs are exponentiated on the FMA pipe: one (causal 8k prompt of 40 heads: 577 us;
-// none 587, two 581 to 584)
+// which of eight score pairs are exponentiated on the FMA pipe: one (causal 8k prompt of 40 heads, replayed in
+// turn: 596 us; none 603)
 constexpr int EMU = 0x10;
 
 struct Ctl {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
           float x0, x1;
           const tc::f2 x = tc::fma2(tc::pack2(s[2 * v], s[2 * v + 1]), sc, ms);
           if ((EMU >> (v & 7)) & 1) {
-            tc::ex2_fma<4>(x, x0, x1);
+            tc::ex2_fma<4, false>(x, x0, x1);
           } else {
             tc::unpack2(x, x0, x1);
             x0 = tc::ex2(x0);
@@ -689,7 +689,7 @@ struct MCtl {
 constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl);
 
 // which of four groups of columns have half of theirs exponentiated on the FMA pipe: one (weights of a
-// 4k prompt: 152 us; none 156, two 154)
+// 4k prompt: 152 us; none 156)
 constexpr int MEMU = 0x1;
 static_assert(MASS_SMEM <= 232448, "shared memory per CTA");
 
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
             const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
             float x0, x1, x2, x3;
             if ((MEMU >> (c & 3)) & 1) {
-              tc::ex2_fma<5>(xa, x0, x1);
+              tc::ex2_fma<5, true>(xa, x0, x1);
             } else {
               tc::unpack2(xa, x0, x1);
               x0 = tc::ex2(x0);

@@ -208,22 +208,31 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   return d;
 }
 
-// max that keeps a NaN
+// max and min that keep a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
 // 2^x of a pair on the FMA pipe, for a share of the exponentials beside the 16 a cycle of the MUFU
 // unit: x = n + f with |f| <= 1/2 (n from adding and subtracting 1.5 * 2^23), 2^f by the polynomial of
 // degree DEG with the least largest relative error on that interval (Remez exchange: 2.6e-6 for 4,
-// 7.5e-8 for 5), n added to the exponent bits.  x below -126 gives 2^-126; x stays below 128.
-template <int DEG>
+// 7.5e-8 for 5), times the power 2^n made from the exponent bits.  x below -126.5 gives exactly 0 (n = -127
+// makes that power 0), 128.5 and more infinity, NaN stays NaN: a factor of the product, where adding n to
+// the bits of 2^f turned NaN into a finite number.  TOP: x may pass 128.
+template <int DEG, bool TOP>
 __device__ __forceinline__ void ex2_fma(f2 x, float &y0, float &y1) {
   float a, b;
   unpack2(x, a, b);
-  x = pack2(max_nan(a, -126.f), max_nan(b, -126.f));
+  a = max_nan(a, -127.f), b = max_nan(b, -127.f);
+  if constexpr (TOP) a = min_nan(a, 128.f), b = min_nan(b, 128.f);
+  x = pack2(a, b);
   const f2 magic = pack2(12582912.f, 12582912.f), back = pack2(-12582912.f, -12582912.f);
   const f2 t = add2(x, magic);
   const f2 f = fma2(add2(t, back), pack2(-1.f, -1.f), x);
@@ -240,11 +249,11 @@ __device__ __forceinline__ void ex2_fma(f2 x, float &y0, float &y1) {
     p = fma2(p, f, pack2(0.6931469440460205f, 0.6931469440460205f));
     p = fma2(p, f, pack2(1.0000001192092896f, 1.0000001192092896f));
   }
-  float p0, p1, t0, t1;
-  unpack2(p, p0, p1);
+  float t0, t1;
   unpack2(t, t0, t1);
-  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+  const float e0 = __uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u),
+              e1 = __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u);
+  unpack2(mul2(p, pack2(e0, e1)), y0, y1);
 }
 
 // true in one lane of the (converged) warp
