@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kvq_codes.cuh"
 #include "kvq_internal.h"
@@ -689,7 +690,7 @@ struct MCtl {
 constexpr int MASS_SMEM = OFF_MCTL + (int)sizeof(MCtl);
 
 // which of four groups of columns have half of theirs exponentiated on the FMA pipe: one (weights of a
-// 4k prompt: 152 us; none 156)
+// 4k prompt: 149 us; none 152)
 constexpr int MEMU = 0x1;
 static_assert(MASS_SMEM <= 232448, "shared memory per CTA");
 
@@ -915,10 +916,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
             for (int c = 0; c < 64; ++c)
               if (c >= from && c < to && (c < c0 || c >= ncol)) s[c] = -INFINITY;
           };
-          auto four = [&](int c) {  // columns 4 c .. 4 c + 3
-            const float4 n4 = nl[c];
-            const tc::f2 xa = tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y));
-            const tc::f2 xb = tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w));
+          auto add = [&](int c, tc::f2 xa, tc::f2 xb) {  // columns 4 c .. 4 c + 3
             float x0, x1, x2, x3;
             if ((MEMU >> (c & 3)) & 1) {
               tc::ex2_fma<5, true>(xa, x0, x1);
@@ -931,33 +929,64 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
             sum[2 * (c & 1)] = tc::add2(sum[2 * (c & 1)], tc::pack2(x0, x1));
             sum[2 * (c & 1) + 1] = tc::add2(sum[2 * (c & 1) + 1], tc::pack2(tc::ex2(x2), tc::ex2(x3)));
           };
-          tc::tmem_ld32(tS, s);
-          tc::tmem_wait_ld();
-          if (ncol > 32) tc::tmem_ld32(tS + 32, s + 32);
-          if (diag || ncol < 32) mask(0, 32);
+          // n columns from group `from` of four on: tiles on the diagonal are masked behind the subtraction,
+          // since the lse of a row that does not see the token may be NaN
+          auto exps = [&](auto masked, int from, int n) {
+            if constexpr (decltype(masked)::value) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) four(c);
-          if (ncol > 32) tc::tmem_wait_ld();
-          tc::fence_before();
-          tc::mbar_arrive_warp(b_se + 8 * b);
-          // the second 32: all of them when nearly full, else in steps of 8
-          if (diag && ncol > 32)
-            mask(32, 64);
-          else if (ncol > 56)
-            mask(56, 64);
-          else if (ncol > 32 && (ncol & 7))
-            mask(32, 64);
-          if (ncol > 56) {
+              for (int u = 0; u < n; ++u) {
+                const int c = from + u;
+                const float4 n4 = nl[c];
+                tc::unpack2(tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y)), s[4 * c], s[4 * c + 1]);
+                tc::unpack2(tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w)), s[4 * c + 2],
+                            s[4 * c + 3]);
+              }
+              mask(4 * from, 4 * (from + n));
 #pragma unroll
-            for (int c = 8; c < 16; ++c) four(c);
-          } else {
+              for (int u = 0; u < n; ++u) {
+                const int c = from + u;
+                add(c, tc::pack2(s[4 * c], s[4 * c + 1]), tc::pack2(s[4 * c + 2], s[4 * c + 3]));
+              }
+            } else {
 #pragma unroll
-            for (int c = 8; c < 14; c += 2) {
-              if (4 * c >= ncol) break;
-              four(c);
-              four(c + 1);
+              for (int u = 0; u < n; ++u) {
+                const int c = from + u;
+                const float4 n4 = nl[c];
+                add(c, tc::fma2(tc::pack2(s[4 * c], s[4 * c + 1]), sc2, tc::pack2(n4.x, n4.y)),
+                    tc::fma2(tc::pack2(s[4 * c + 2], s[4 * c + 3]), sc2, tc::pack2(n4.z, n4.w)));
+              }
             }
-          }
+          };
+          auto tile = [&](auto masked) {
+            constexpr bool late = decltype(masked)::value;
+            tc::tmem_ld32(tS, s);
+            tc::tmem_wait_ld();
+            if (ncol > 32) tc::tmem_ld32(tS + 32, s + 32);
+            if (!late && ncol < 32) mask(0, 32);
+            exps(masked, 0, 8);
+            if (ncol > 32) tc::tmem_wait_ld();
+            tc::fence_before();
+            tc::mbar_arrive_warp(b_se + 8 * b);
+            // the second 32: all of them when nearly full, else in steps of 8
+            if (!late) {
+              if (ncol > 56)
+                mask(56, 64);
+            }
+            if (ncol > 56) {
+              exps(masked, 8, 8);
+            } else {
+#pragma unroll
+              for (int c = 8; c < 14; c += 2) {
+                if (4 * c >= ncol) break;
+                if (!late && 4 * c + 8 > ncol) mask(4 * c, 4 * c + 8);
+                exps(masked, c, 2);
+              }
+            }
+          };
+          if (__builtin_expect(!diag, 1))
+            tile(std::false_type{});
+          else
+            tile(std::true_type{});
           float v0, v1;
           tc::unpack2(tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3])), v0, v1);
           const float v = v0 + v1, w = total + v, d = w - total;

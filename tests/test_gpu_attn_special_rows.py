@@ -78,6 +78,22 @@ def test_tokens_a_row_does_not_see_get_exactly_zero():
         assert t.equal(kept[0, 0].long().cpu(), t.arange(keep)), row
 
 
+def test_a_nan_row_does_not_reach_the_tokens_it_does_not_see():
+    t = P.torch()
+    n, G = 300, 2
+    k, v = P.kv(4, [n], 1)
+    c = P.cache("bf16", [n], 1, k, v)
+    q = P.queries(4, n, G, t.bfloat16)
+    _, lse = c.batch_attn(0, [0], [n], q, causal=True, return_lse=True)
+    want = weigh(c, q, lse, True)
+    for row in (0, 5, 63, 64, 100, 127, 128, 191, 250, 298):
+        bad = lse.clone()
+        bad[row, 1] = math.nan
+        got = weigh(c, q, bad, True)
+        assert bool(t.isnan(got[..., : row + 1]).all()), row
+        assert t.equal(got[..., row + 1:], want[..., row + 1:]), row
+
+
 @pytest.mark.parametrize("m,G", [(200, 1), (60, 5)])
 def test_masked_values_add_nothing_however_large(m, G):
     """Values near the largest BF16 number in tokens that the first rows of a prompt do not see."""
