@@ -88,10 +88,11 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //    rescaled in tensor memory then), so most tiles need no correction and the two threads of a row
 //    only agree, by one barrier with an OR, that none is due.
 // Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
-// Calls of few rows (ONE) over up to ONE_TOKENS tokens, which latency bounds, multiply the weights'
-// remainders too and are as exact as their output's type; with two tiles that costs 6 % and more (causal
-// 8k prompt 613 us for 577), over long contexts power (one row over 65 536 tokens, many calls in a row:
-// 59.9 us for 56.0).
+// Entries whose rows fill no more than one tile, which latency or HBM bounds, multiply the weights' remainders
+// too and are as exact as their output's type, whatever else is in the call (replays, rounded weights and then
+// these, BF16, 8 KV heads: one row over 4096 tokens 15.2 and 16.5 us, 16 384: 23.1 and 24.8, 65 536: 54.7 and
+// 55.3, 131 072: 94.8 and 94.0; 400 calls in a row, which the power limit slows: 65 536: 54.9 and 55.7, 131 072:
+// 98 and 108).  With two tiles they cost 6 % and more (causal 8k prompt 613 us for 577).
 // Bound, many rows: the chain scores -> maximum -> exponentials -> weights of a tile against the other
 // group's products (causal 8k prompt of 40 heads, F16: 577 us, 1190 TFLOP/s; tensor pipe 53 %, exponentials
 // 48 %).  Bound, one row: HBM (65 536 tokens, 268 MB: 48 us + the join, 5.0 TB/s).
@@ -104,7 +105,6 @@ constexpr int NT = 576;
 constexpr int TILE = BT * D * 2;   // bytes of a tile
 constexpr int HALF = TILE / 2;     // 64 channels of it
 constexpr int MAXST = 6;           // stages
-constexpr int ONE_TOKENS = 16384;
 constexpr float TAU = 8.f;         // lazy maximum, log2 units
 constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
 constexpr int MAXSPL = 64;
@@ -145,9 +145,10 @@ struct Ring {
   }
 };
 
-// LO: the keys have remainders (a rebuilt cache).  ONE: no entry has more than one tile of query rows, nor
-// more than ONE_TOKENS tokens.
-template <bool F16, bool LO, bool ONE>
+// LO: the keys have remainders (a rebuilt cache).  ROWS: the query rows of no entry (ONE) or of every entry
+// (MORE) fill more than one tile, or of some (ANY: the choice of the weights by entry costs 6 % of MORE).
+enum Rows { ONE, MORE, ANY };
+template <bool F16, bool LO, Rows ROWS>
 __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
                                                 const __grid_constant__ CUtensorMap qmap,
                                                 const __grid_constant__ BArgs A) {
@@ -172,7 +173,8 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   const int sp = local % e.nsplit, head = local / e.nsplit % A.hkv;
   const int blk = e.nblk - 1 - local / e.nsplit / A.hkv;  // the last (causal: longest) first
   const int tok0 = blk * 2 * TB, tok1 = min(e.nq, tok0 + 2 * TB);
-  const bool halves = ONE || tok1 - tok0 <= TB;
+  const bool halves = ROWS == ONE || tok1 - tok0 <= TB;
+  const bool rem = ROWS == ONE || (ROWS == ANY && e.nq <= TB);  // the weights' remainders are multiplied too
   const int ntile = halves ? 1 : 2;  // query tiles
   const int64_t lim_max = limit_of(A, e, tok1 - 1);
   const int kt = (int)((lim_max + BT - 1) / BT);
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
             for (int s = 0; s < 4; ++s)
               tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 8 * s, v + (uint64_t)((4 * h + s) * (2048 >> 4)), idO,
                          h == 0 && s == 0 ? acc : 1u);
-            if (ONE) {
+            if (rem) {
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 32 + 8 * s,
@@ -454,15 +456,15 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       const float sub = m == -INFINITY ? 0.f : -m;
       const tc::f2 sc = tc::pack2(A.qscale, A.qscale), ms = tc::pack2(sub, sub);
       tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
-      // P over the scores this thread has read; with ONE the weights' remainders behind it
-      if constexpr (ONE) {
+      // P over the scores this thread has read; where they count the weights' remainders behind it
+      if (rem) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[16], lo16[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t hi[8], lo16[8];
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
+          for (int v = 0; v < 8; ++v) {
             float x0, x1;
-            const int at = 32 * c + 2 * v;
+            const int at = 16 * c + 2 * v;
             tc::unpack2(tc::fma2(tc::pack2(s[at], s[at + 1]), sc, ms), x0, x1);
             x0 = tc::ex2(x0);
             x1 = tc::ex2(x1);
@@ -471,8 +473,8 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
             const float2 f = tc::widen2<F16>(hi[v]);
             lo16[v] = tc::round2<F16>(x0 - f.x, x1 - f.y);
           }
-          tc::tmem_st16(tS + 16 * c, hi);
-          tc::tmem_st16(tS + 32 + 16 * c, lo16);
+          tc::tmem_st8(tS + 8 * c, hi);
+          tc::tmem_st8(tS + 32 + 8 * c, lo16);
         }
       } else {
         uint32_t w[32];
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       tc::fence_after();
     }
     // halves: group 1 leaves its own in the stages (all consumed), group 0 joins the two
-    const bool one = ONE || C.halves, join = one && tiles > 1, split = C.nsplit > 1;
+    const bool one = ROWS == ONE || C.halves, join = one && tiles > 1, split = C.nsplit > 1;
     float *ex = reinterpret_cast<float *>(S + (one ? 1 : 2) * TILE);  // [128 rows][129], then m and l
     if (join && t == 1) {
 #pragma unroll 1
@@ -1480,18 +1482,24 @@ bool launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t s
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <bool F16, bool LO, bool ONE>
+template <bool F16, bool LO, Rows ROWS>
 int run_attn(const CUtensorMap &map, const CUtensorMap &qmap, const BArgs &A, unsigned ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(k_attn<F16, LO, ONE>, ATTN_SMEM, done)) return KVQ_E_CUDA;
+  if (!allow_smem(k_attn<F16, LO, ROWS>, ATTN_SMEM, done)) return KVQ_E_CUDA;
   if (LO) {  // set up behind the rebuild (64 rows over 4096 q8_0 tokens: 62.8 -> 59.4 us)
-    if (!launch_behind(k_attn<F16, LO, ONE>, ctas, NT, ATTN_SMEM, st, map, qmap, A)) return KVQ_E_CUDA;
+    if (!launch_behind(k_attn<F16, LO, ROWS>, ctas, NT, ATTN_SMEM, st, map, qmap, A)) return KVQ_E_CUDA;
   } else {
-    k_attn<F16, LO, ONE><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
+    k_attn<F16, LO, ROWS><<<ctas, NT, ATTN_SMEM, st>>>(map, qmap, A);
     if (cudaGetLastError() != cudaSuccess) return KVQ_E_CUDA;
   }
   note_launches(1);
   return KVQ_OK;
+}
+
+// by whether some entries have no more than one tile of query rows, and some more
+template <bool F16, bool LO>
+auto pick_attn(bool one, bool more) {
+  return !more ? run_attn<F16, LO, ONE> : (one ? run_attn<F16, LO, ANY> : run_attn<F16, LO, MORE>);
 }
 
 template <bool F16>
@@ -1550,12 +1558,12 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   for (size_t base = 0; base < P.e.size(); base += MAXE) {
     const int ne = (int)std::min<size_t>(MAXE, P.e.size() - base);
     int64_t ctas = 0, joins = 0;
-    bool one = true;
+    bool one = false, more = false;
     A.ne = 0;
     for (int i = 0; i < ne; ++i) {
       BEntry e = P.e[base + i];
       if (e.nq == 0) continue;
-      one = one && e.nq <= BT / A.G && e.n <= ONE_TOKENS;
+      (e.nq <= BT / A.G ? one : more) = true;
       e.cta0 = (int)ctas;
       ctas += (int64_t)e.nblk * A.hkv * e.nsplit;
       if (e.nsplit > 1) joins += (int64_t)e.nq * n_q_heads;
@@ -1563,10 +1571,8 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
     }
     if (ctas == 0) continue;
     if (ctas > INT32_MAX) return KVQ_E_UNSUPPORTED;
-    const auto run = one ? (A.src.sides == 3 ? run_attn<true, true, true>
-                                             : (A.src.f16 ? run_attn<true, false, true> : run_attn<false, false, true>))
-                         : (A.src.sides == 3 ? run_attn<true, true, false>
-                                             : (A.src.f16 ? run_attn<true, false, false> : run_attn<false, false, false>));
+    const auto run = A.src.sides == 3 ? pick_attn<true, true>(one, more)
+                                      : (A.src.f16 ? pick_attn<true, false>(one, more) : pick_attn<false, false>(one, more));
     if (const int rc = run(map, qmap, A, (unsigned)ctas, st)) return rc;
     if (joins == 0) continue;
     if (joins > INT32_MAX) return KVQ_E_UNSUPPORTED;

@@ -37,3 +37,43 @@ def test_every_tile_is_where_it_belongs(n, m, causal, f16):
 def test_every_tile_of_a_rebuilt_cache(type_):
     run(type_, [5001, 300], [3, 60], 2, 5, False, seed=3, tail=128)
     run(type_, [2100], [140], 1, 5, True, seed=4)
+
+
+def faint(n, count, f16):
+    """A flat background below one peak in every 128 tokens (so that no part of the row's weights is relative to
+    the background): count rows x 5 heads whose background's scores lie (row * 5 + head) / 32 below the
+    peaks'.  -> q, k, v of one KV head, exact out"""
+    t = P.torch()
+    q = t.zeros(count, 5, 128)
+    q[..., 0] = t.arange(1, 5 * count + 1).view(count, 5) / 32
+    k, v = t.zeros(n, 1, 128), t.full((n, 1, 128), 1.25)
+    k[::128, 0, 0] = 1.0
+    v[::128] = 0.0
+    peaks = -(-n // 128)
+    w = (n - peaks) * t.exp(-q[..., 0].double())
+    out = 1.25 * w / (peaks + w)
+    return q.to(t.float16 if f16 else t.bfloat16).cuda(), k.bfloat16().cuda(), v.bfloat16().cuda(), out.cuda()
+
+
+@pytest.mark.parametrize("f16", [0, 1])
+@pytest.mark.parametrize("company", ["none", "rows", "tokens", "both"])
+def test_few_rows_are_as_exact_as_their_type_whatever_else_is_in_the_call(company, f16):
+    t = P.torch()
+    n = 1000
+    q, k, v, want = faint(n, 25, f16)
+    lens, n_q, extra = [n], [25], 0
+    if company in ("tokens", "both"):
+        lens, n_q, extra = lens + [20000], n_q + [1], extra + 1
+    if company in ("rows", "both"):
+        lens, n_q, extra = lens + [400], n_q + [90], extra + 90
+    k2, v2 = P.kv(1, [max(sum(lens[1:]), 1)], 1)
+    c = P.cache("bf16", lens, 1, t.cat([k, k2])[:sum(lens)], t.cat([v, v2])[:sum(lens)], tail_f16=f16)
+    qs = t.cat([q, P.queries(2, extra, 5, q.dtype)]) if extra else q
+    out = c.batch_attn(0, list(range(len(lens))), n_q, qs, softmax_scale=1.0)[:25].double()
+    assert c.status() == 0
+    # the scores are exact; exp's few steps, one step a sum, the remainders' rounding; then the output's half step
+    rel = 16 * P.U32 + (n + 16) * 2 * P.U32 + (P.U16 if f16 else P.UB16) ** 2
+    want = want[..., None]
+    tol = rel * want + P.half_step(q.dtype) * want * (1 + rel)
+    err = (out - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
