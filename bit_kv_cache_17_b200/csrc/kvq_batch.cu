@@ -87,7 +87,9 @@ __device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4])
 //  - the running maximum moves only when a score passes it by 2^8 (the weights stay below 2^8, O is
 //    rescaled in tensor memory then), so most tiles need no correction and the two threads of a row
 //    only agree, by one barrier with an OR, that none is due.
-// Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.
+// Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.  F16 weights
+// are 2^7 times as large (below 2^15): what falls under the normal range there is off by 2^-32 of the row's
+// largest weight at most, not 2^-25, which many faint tokens would add up (l, O and the records know nothing of it).
 // Entries whose rows fill no more than one tile, which latency or HBM bounds, multiply the weights' remainders
 // too and are as exact as their output's type, whatever else is in the call (replays, rounded weights and then
 // these, BF16, 8 KV heads: one row over 4096 tokens 15.2 and 16.5 us, 16 384: 23.1 and 24.8, 65 536: 54.7 and
@@ -106,6 +108,7 @@ constexpr int TILE = BT * D * 2;   // bytes of a tile
 constexpr int HALF = TILE / 2;     // 64 channels of it
 constexpr int MAXST = 6;           // stages
 constexpr float TAU = 8.f;         // lazy maximum, log2 units
+constexpr float LIFT = 7.f;        // of F16 weights, log2 units
 constexpr int PREC = 4 + D;        // floats of a partial record: m, l, -, -, acc
 constexpr int MAXSPL = 64;
 constexpr int EXG = BT * 129 + 2 * BT;  // floats a group leaves in the stages at the end (rows padded to 129)
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         tc::bar_sync(pair, 64);
         tc::fence_after();
       }
-      const float sub = m == -INFINITY ? 0.f : -m;
+      const float sub = m == -INFINITY ? 0.f : (F16 ? LIFT - m : -m);
       const tc::f2 sc = tc::pack2(A.qscale, A.qscale), ms = tc::pack2(sub, sub);
       tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
       // P over the scores this thread has read; where they count the weights' remainders behind it
@@ -504,7 +507,8 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     // ---- the result: m, l of the row, 64 channels of the accumulator
     C.row[t][h][r] = l;
     tc::bar_sync(pair, 64);
-    l = C.row[t][0][r] + C.row[t][1][r];
+    constexpr float back = F16 ? 1.f / (1 << (int)LIFT) : 1.f;
+    l = (C.row[t][0][r] + C.row[t][1][r]) * back;
     const int tiles = C.nt;
     if (tiles > 0) {
       tc::mbar_wait(b_o, 0, abort, A.status);
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       }
       // a split's rows in fp32, behind what the other group left; otherwise through the query tile (no
       // product reads it any more), in its layout
-      const float inv = split ? 1.f : (l > 0.f ? 1.f / l : (l == l ? 0.f : l));
+      const float inv = split ? back : (l > 0.f ? back / l : (l == l ? 0.f : l));
       float *part = ex + (one ? 1 : t) * EXG;
       uint8_t *qt = S + t * TILE;
 #pragma unroll 1
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
         }
         if (split) {
 #pragma unroll
-          for (int v = 0; v < 32; ++v) part[r * 129 + ch + v] = o[v];
+          for (int v = 0; v < 32; ++v) part[r * 129 + ch + v] = o[v] * inv;
         } else {
           uint8_t *dst = qt + h * HALF + r * 128;
 #pragma unroll

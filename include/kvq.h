@@ -326,7 +326,7 @@ int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs,
  * workspace: device, >= kvq_batch_workspace_bytes (NULL where that is 0); calls that may overlap on
  * the GPU need workspaces of their own, and may otherwise run at the same time, the cache being only
  * read.  Scores, the softmax and both sums are fp32; the weights are rounded to the 16-bit type of the
- * matrix product, and entries of at most floor(128 / G) query tokens (G query heads per KV head) have
+ * matrix product (F16 ones below their normal range to 2^-32 of the row's largest), and entries of at most floor(128 / G) query tokens (G query heads per KV head) have
  * their remainders multiplied too, which leaves the output's own rounding.  A BF16 cache (either tail format) is read as it is; a quantized cache is first
  * rebuilt in the original basis in the workspace, keys as F16 high part and remainder, values as F16
  * (values and queries must then lie within the F16 range).  kvq_decode_attn remains the call for one

@@ -1,4 +1,6 @@
 """Batch attention held to bounds that see one wrong tile and one rounding too many."""
+import math
+
 import pytest
 
 import attn_bounds as B
@@ -77,3 +79,33 @@ def test_few_rows_are_as_exact_as_their_type_whatever_else_is_in_the_call(compan
     tol = rel * want + P.half_step(q.dtype) * want * (1 + rel)
     err = (out - want).abs()
     assert bool((err <= tol).all()), float((err - tol).max())
+
+
+@pytest.mark.parametrize("type_", ["f16", "q8_0"])
+@pytest.mark.parametrize("n_q", [[25] * 20, [1000]])
+def test_many_faint_tokens_add_up(n_q, type_):
+    """65 536 tokens 17.5 below a peak in front of them: each weight is under half of the least F16 number.  As
+    many rows as leave the context in one piece (a piece without the peak has no small weights)."""
+    t = P.torch()
+    n, m, f16 = 65536, sum(n_q), int(type_ == "f16")
+    q = t.zeros(m, 40, 128)
+    q[..., 0] = 17.5
+    k, v = t.zeros(n, 8, 128), t.ones(n, 8, 128)
+    peaks = 2  # in the first two tiles, which calls of few rows take separately
+    k[0, :, 0] = k[128, :, 0] = 1.0
+    v[0] = v[128] = 0.0
+    c = P.cache("bf16" if f16 else type_, [n], 8, k.bfloat16().cuda(), v.bfloat16().cuda(), tail_f16=f16)
+    q = q.to(t.float16 if f16 else t.bfloat16).cuda()
+    out = c.batch_attn(0, [0] * len(n_q), n_q, q, softmax_scale=1.0)
+    assert c.status() == 0
+    key, value = (float(x[i, 0, 0]) for x, i in zip(P.cached(c, 0, 0), (0, 1)))
+    w = (n - peaks) * math.exp(-17.5 * key)
+    want = value * w / (peaks + w)
+    # the score is one product (and, rebuilt, a key of 22 bits); a weight below the normal range is off by 2^-25
+    # of 2^7 or more; a step of fp32 for every addition; the value's rounding
+    rel = 2 * 17.5 * (4 * P.U32 + (0.0 if f16 else 2.0 ** -22)) + (n + 16) * 2 * P.U32 + (0.0 if f16 else P.U16)
+    tol = rel * want + n * 2.0 ** -32
+    tol = tol + P.half_step(q.dtype) * (want + tol) + 2.0 ** -25
+    assert want > 8 * tol
+    err = (out.double() - want).abs().amax()
+    assert float(err) <= tol, (want, float(err), tol)
