@@ -12,6 +12,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "kvq_internal.h"
 
@@ -303,6 +304,23 @@ int check_rows(int64_t n, int heads, const void *x, int ti, int64_t ld, const vo
   return x0 < y1 && y0 < x1 ? KVQ_E_INVAL : KVQ_OK;
 }
 
+// Rows of one tensor: n of `width` bytes, `stride` apart (at least the width).
+struct Rows {
+  uintptr_t at;
+  uint64_t width, stride;
+};
+
+// Whether n rows of a and n of b share a byte.  Of one stride (slices of a packed row) they may interleave:
+// what counts then is where b lies within a's row.
+bool rows_overlap(int64_t n, Rows a, Rows b) {
+  if (b.at < a.at) std::swap(a, b);
+  const uint64_t apart = b.at - a.at;
+  if (apart >= (uint64_t)(n - 1) * a.stride + a.width) return false;
+  if (n == 1 || a.stride != b.stride) return true;
+  const uint64_t within = apart % a.stride;
+  return within < a.width || a.stride - within < b.width;
+}
+
 template <bool VEC>
 cudaError_t run(int qi, int qo, unsigned grid, size_t smem, cudaStream_t st, const RopeArgs &A) {
 #define KVQ_ROPE(I, O)                                    \
@@ -352,6 +370,20 @@ extern "C" int kvq_rope(const kvq_rope_params *p, const double *inv_freq, int64_
   int rc = check_rows(n_tokens, n_q_heads, q, q_type, q_ld, q_out, q_out_type, q_out_ld);
   if (rc == KVQ_OK) rc = check_rows(n_tokens, n_k_heads, k, KVQ_DT_BF16, k_ld, k_out, KVQ_DT_BF16, k_out_ld);
   if (rc) return rc;
+  // an output over another tensor's rows, or over the positions: other blocks still read (or write) those
+  const auto rows = [](const void *x, int heads, int type, int64_t ld) {
+    return Rows{(uintptr_t)x, (uint64_t)heads * D * elem_bytes(type), (uint64_t)ld * elem_bytes(type)};
+  };
+  const Rows rq = rows(q, n_q_heads, q_type, q_ld), rqo = rows(q_out, n_q_heads, q_out_type, q_out_ld);
+  const Rows rk = rows(k, n_k_heads, KVQ_DT_BF16, k_ld), rko = rows(k_out, n_k_heads, KVQ_DT_BF16, k_out_ld);
+  if (n_q_heads && n_k_heads &&
+      (rows_overlap(n_tokens, rqo, rk) || rows_overlap(n_tokens, rko, rq) || rows_overlap(n_tokens, rqo, rko)))
+    return KVQ_E_INVAL;
+  const uint64_t pos_bytes = (uint64_t)((p->n_axes - 1) * pos_ld + n_tokens) * sizeof(int32_t);
+  const auto over_pos = [&](const Rows &r) {
+    return overlap(pos, pos_bytes, (const void *)r.at, (uint64_t)(n_tokens - 1) * r.stride + r.width);
+  };
+  if ((n_q_heads && over_pos(rqo)) || (n_k_heads && over_pos(rko))) return KVQ_E_INVAL;
 
   RopeArgs A{};
   int left[4] = {0, 0, 0, 0}, a = 0;

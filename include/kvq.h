@@ -298,11 +298,14 @@ void kvq_rope_default_params(kvq_rope_params *p);
  * pos: device int32, pos[a * pos_ld + t] the position of token t on axis a (any value; the angle is
  * reduced in 64 bits); pos_ld is 0 (one row for all axes, text tokens) or >= n_tokens.
  * q: device rows [n_tokens][n_q_heads][128] of q_type, token t at element t * q_ld (a slice of a
- * packed q|k|v row is a q_ld larger than n_q_heads * 128); q_out likewise, of q_out_type.  k, k_out: BF16 rows, as kvq_append takes them.  n_q_heads or n_k_heads may be 0 (its
- * pointers are then not looked at).  An output may be its own input (same type and ld); otherwise
- * the spans from the first to the last row of the two must not overlap (KVQ_E_INVAL).  Pointers and
- * row strides are multiples of 16 bytes (KVQ_E_ALIGN; pos: 4).  Arithmetic is fp32 with one rounding
- * to the output type; channels that pass through are converted only.  Runs on the current device. */
+ * packed q|k|v row is a q_ld larger than n_q_heads * 128); q_out likewise, of q_out_type.  k, k_out:
+ * BF16 rows, as kvq_append takes them.  n_q_heads or n_k_heads may be 0 (its pointers are then not
+ * looked at).  An output may be its own input (same type and ld); otherwise the spans from the first to
+ * the last row of the two must not overlap (KVQ_E_INVAL).  Neither may an output share a byte with the
+ * other tensor's input or output (rows of one stride may interleave, as slices of a packed row do; of
+ * different strides their spans count) or its span with pos (KVQ_E_INVAL).  Pointers and row strides
+ * are multiples of 16 bytes (KVQ_E_ALIGN; pos: 4).  Arithmetic is fp32 with one rounding to the output
+ * type; channels that pass through are converted only.  Runs on the current device. */
 int kvq_rope(const kvq_rope_params *p, const double *inv_freq, int64_t n_tokens, const int32_t *pos,
              int64_t pos_ld, int32_t n_q_heads, const void *q, int32_t q_type, int64_t q_ld, void *q_out,
              int32_t q_out_type, int64_t q_out_ld, int32_t n_k_heads, const void *k, int64_t k_ld,
@@ -326,9 +329,10 @@ int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs,
  * workspace: device, >= kvq_batch_workspace_bytes (NULL where that is 0); calls that may overlap on
  * the GPU need workspaces of their own, and may otherwise run at the same time, the cache being only
  * read.  Scores, the softmax and both sums are fp32; the weights are rounded to the 16-bit type of the
- * matrix product (F16 ones below their normal range to 2^-32 of the row's largest), and entries of at most floor(128 / G) query tokens (G query heads per KV head) have
- * their remainders multiplied too, which leaves the output's own rounding.  A BF16 cache (either tail format) is read as it is; a quantized cache is first
- * rebuilt in the original basis in the workspace, keys as F16 high part and remainder, values as F16
+ * matrix product (F16 ones below their normal range to 2^-32 of the row's largest), and entries of at
+ * most floor(128 / G) query tokens (G query heads per KV head) have their remainders multiplied too,
+ * which leaves the output's own rounding.  A BF16 cache (either tail format) is read as it is; a
+ * quantized cache is first rebuilt in the original basis in the workspace, keys as F16 high part and remainder, values as F16
  * (values and queries must then lie within the F16 range).  kvq_decode_attn remains the call for one
  * fp32 query row per quantized sequence.  The same call gives the same bits whatever else runs: every
  * sum has a fixed order.  How a long context is split, and so an entry's last bits, depends on which
