@@ -1540,7 +1540,10 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   if (!q || !out || (!workspace && P.bytes > 0)) return KVQ_E_INVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace)) return KVQ_E_ALIGN;
   const uint64_t row_bytes = (uint64_t)P.rows * n_q_heads * D * 2;
-  if (overlap(q, row_bytes, out, row_bytes)) return KVQ_E_INVAL;
+  const uint64_t lse_bytes = (uint64_t)P.rows * n_q_heads * sizeof(float);
+  if (overlap(q, row_bytes, out, row_bytes) || overlap(lse, lse_bytes, q, row_bytes) ||
+      overlap(lse, lse_bytes, out, row_bytes))
+    return KVQ_E_INVAL;
   if (ws_bytes < P.bytes) return KVQ_E_SIZE;
   if (const int rc = check_device(c)) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -1605,6 +1608,9 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   if (mass_ld < most || mass_ld > INT64_MAX / 8 / mass_rows) return KVQ_E_INVAL;
   const uint64_t mass_bytes = (uint64_t)(mass_rows * mass_ld) * sizeof(float);
   if (decay != 0.f && mass_in != mass_out && overlap(mass_in, mass_bytes, mass_out, mass_bytes)) return KVQ_E_INVAL;
+  const uint64_t row_values = (uint64_t)P.rows * n_q_heads;
+  if (overlap(mass_out, mass_bytes, lse, row_values * sizeof(float)) || overlap(mass_out, mass_bytes, q, row_values * D * 2))
+    return KVQ_E_INVAL;
   if (!aligned16(q) || !aligned16(lse) || !aligned16(mass_in) || !aligned16(mass_out) || !aligned16(workspace))
     return KVQ_E_ALIGN;
   if (ws_bytes < P.bytes) return KVQ_E_SIZE;

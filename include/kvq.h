@@ -322,8 +322,9 @@ int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs,
  * tokens, n_q[e] <= n).  Entry e is n_q[e] >= 0 query tokens over sequence seq_ids[e]; a sequence may
  * be listed several times (beams over one encoder state).
  * q: device [sum(n_q), n_q_heads, 128] in the cache's 16-bit format (BF16, or F16 with tail_f16),
- * the rows of entry 0 first; out: same shape and type, sharing no byte with q (KVQ_E_INVAL); lse:
- * device fp32 [sum(n_q), n_q_heads] or NULL: log of the sum of exp(scale q.k) of each row.  softmax_scale <= 0 selects 1/sqrt(128).
+ * the rows of entry 0 first; out: same shape and type; lse: device fp32 [sum(n_q), n_q_heads] or NULL:
+ * log of the sum of exp(scale q.k) of each row.  No two of q, out and lse may share a byte (KVQ_E_INVAL).
+ * softmax_scale <= 0 selects 1/sqrt(128).
  * A row that sees no token gives zeros and lse = -inf.  Cached values must be finite (a value that is
  * not reaches every row that attends to its 128-token tile, also where the row does not see it).
  * workspace: device, >= kvq_batch_workspace_bytes (NULL where that is 0); calls that may overlap on
@@ -345,9 +346,10 @@ int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *s
  * mass_out[e][h][t] = decay * mass_in[e][h][t] + sum over the rows of entry e and the query heads
  * of KV head h that see token t of exp(scale q.k - lse), for t < n; places behind the sequence's
  * last token are left as they were.  mass_in, mass_out: device fp32, [n_seqs][n_kv_heads][mass_ld],
- * mass_ld >= the longest listed sequence; mass_out may be mass_in, and may not overlap it otherwise
- * (KVQ_E_INVAL); decay in [0, 1], and with decay 0 mass_in is not read (NULL allowed).  lse: as
- * kvq_batch_attn (or any call over the same rows) wrote it; rows with lse = -inf weigh nothing.  The other arguments are kvq_batch_attn's. */
+ * mass_ld >= the longest listed sequence; mass_out may be mass_in, and may not overlap it otherwise, nor
+ * q or lse (KVQ_E_INVAL); decay in [0, 1], and with decay 0 mass_in is not read (NULL allowed).  lse: as
+ * kvq_batch_attn (or any call over the same rows) wrote it; rows with lse = -inf weigh nothing.  The
+ * other arguments are kvq_batch_attn's. */
 int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids, const int32_t *n_q,
                   int32_t n_q_heads, int32_t causal, const void *q, float softmax_scale, const float *lse,
                   float decay, const float *mass_in, float *mass_out, int64_t mass_ld, void *workspace,
