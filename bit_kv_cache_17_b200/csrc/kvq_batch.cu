@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
           float x0, x1;
           const tc::f2 x = tc::fma2(tc::pack2(s[2 * v], s[2 * v + 1]), sc, ms);
           if ((EMU >> (v & 7)) & 1) {
-            tc::ex2_fma<4, false>(x, x0, x1);
+            tc::ex2_fma<false>(x, x0, x1);
           } else {
             tc::unpack2(x, x0, x1);
             x0 = tc::ex2(x0);
@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
           auto add = [&](int c, tc::f2 xa, tc::f2 xb) {  // columns 4 c .. 4 c + 3
             float x0, x1, x2, x3;
             if ((MEMU >> (c & 3)) & 1) {
-              tc::ex2_fma<5, true>(xa, x0, x1);
+              tc::ex2_fma<true>(xa, x0, x1);
             } else {
               tc::unpack2(xa, x0, x1);
               x0 = tc::ex2(x0);
