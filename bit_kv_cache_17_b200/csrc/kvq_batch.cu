@@ -1002,14 +1002,15 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
         if (!resident) tc::mbar_arrive_warp(b_qe + 8 * st);
       }
       // the second half hands its sum over and goes on, the first one writes
+      if (total != INFINITY) total += rest;  // (of an infinite sum the rest is NaN)
       const uint32_t hb = 8 * (4 * t + (warp & 3));
       if (h == 1) {
         if (p > p0) tc::mbar_wait(b_he + hb, (p - p0 - 1) & 1, abort, A.status);
-        C.half[t][r] = total + rest;
+        C.half[t][r] = total;
         tc::mbar_arrive_warp(b_hf + hb);
       } else {
         tc::mbar_wait(b_hf + hb, (p - p0) & 1, abort, A.status);
-        const float v = total + rest + C.half[t][r];
+        const float v = total + C.half[t][r];
         tc::mbar_arrive_warp(b_he + hb);
         if (key < n) {
           if (e.mqs > 1) {

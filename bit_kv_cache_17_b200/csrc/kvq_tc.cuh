@@ -229,7 +229,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // unit: x = n + f with |f| <= 1/2 (n from adding and subtracting 1.5 * 2^23), 2^f by the polynomial of
 // degree 5 with the least largest relative error on that interval (Remez exchange: 7.5e-8; degree 4, 2.6e-6,
 // was no faster: causal 8k prompt of 40 heads 594 us for 592), times the power 2^n made from the exponent bits.  x below -126.5 gives exactly 0 (n = -127
-// makes that power 0), 128.5 and more infinity, NaN stays NaN: a factor of the product, where adding n to
+// makes that power 0), 127.5 and more infinity, NaN stays NaN: a factor of the product, where adding n to
 // the bits of 2^f turned NaN into a finite number.  TOP: x may pass 128.
 template <bool TOP>
 __device__ __forceinline__ void ex2_fma(f2 x, float &y0, float &y1) {

@@ -58,6 +58,19 @@ def test_rows_that_weigh_nothing_add_exactly_zero(type_, causal, low):
     assert t.equal(weigh(c, q, lse, causal, decay=1.0, mass_in=prev), prev)
 
 
+def test_a_weight_past_the_range_is_infinite_in_every_column():
+    """Rows whose lse does not belong to their scores, at each place of a tile in turn."""
+    t = P.torch()
+    k, v = P.kv(6, [130], 1)
+    c = P.cache("bf16", [130], 1, k, v)
+    q = P.queries(6, 25, 5, t.bfloat16)
+    for low in (-200.0, -3e38):
+        for i in range(25):
+            lse = t.full((25, 5), -math.inf, device="cuda")
+            lse[i, i % 5] = low
+            assert bool((weigh(c, q, lse) == math.inf).all()), (low, i)
+
+
 def test_tokens_a_row_does_not_see_get_exactly_zero():
     """Causal, one row with weight: the tokens behind it get nothing from it, and keep their order of index
     where an eviction has to choose among them."""
