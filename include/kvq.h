@@ -329,15 +329,18 @@ int kvq_batch_workspace_bytes(const kvq_cache *c, int32_t layer, int32_t n_seqs,
  * not reaches every row that attends to its 128-token tile, also where the row does not see it).
  * workspace: device, >= kvq_batch_workspace_bytes (NULL where that is 0); calls that may overlap on
  * the GPU need workspaces of their own, and may otherwise run at the same time, the cache being only
- * read.  Scores, the softmax and both sums are fp32; the weights are rounded to the 16-bit type of the
- * matrix product (F16 ones below their normal range to 2^-32 of the row's largest), and entries of at
- * most floor(128 / G) query tokens (G query heads per KV head) have their remainders multiplied too,
- * which leaves the output's own rounding.  A BF16 cache (either tail format) is read as it is; a
- * quantized cache is first rebuilt in the original basis in the workspace, keys as F16 high part and remainder, values as F16
- * (values and queries must then lie within the F16 range).  kvq_decode_attn remains the call for one
- * fp32 query row per quantized sequence.  The same call gives the same bits whatever else runs: every
- * sum has a fixed order.  How a long context is split, and so an entry's last bits, depends on which
- * entries the call lists, their lengths and their counts. */
+ * read.
+ * Scores, the softmax (exponentials within 4e-7 of their value) and both sums are fp32; the weights are
+ * rounded to the 16-bit type of the matrix product (F16 ones below their normal range to 2^-32 of the
+ * row's largest), and entries of at most floor(128 / G) query tokens (G query heads per KV head) have
+ * their remainders multiplied too, which leaves the output's own rounding.
+ * A BF16 cache (either tail format) is read as it is; a quantized cache is first rebuilt in the original
+ * basis in the workspace, keys as F16 high part and remainder, values as F16, and BF16 queries are
+ * converted to F16.  Keys, values and queries must then lie within the F16 range: one of 65520 or more
+ * makes the rows that meet it NaN or infinite, and what is below 2^-25 in a query or value counts as 0.
+ * kvq_decode_attn remains the call for one fp32 query row per quantized sequence.
+ * The same call gives the same bits whatever else runs: every sum has a fixed order.  How a long context
+ * is split, and with it an entry's last bits, depends on the entries that the call lists. */
 int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const int32_t *seq_ids, const int32_t *n_q,
                    int32_t n_q_heads, int32_t causal, const void *q, float softmax_scale, void *out, float *lse,
                    void *workspace, size_t ws_bytes, kvq_stream_t stream);

@@ -119,3 +119,20 @@ def test_masked_values_add_nothing_however_large(m, G):
     q = P.queries(5, m, G, t.bfloat16)
     a, b = (P.cache("bf16", [n], 1, k, x).batch_attn(0, [0], [m], q, causal=True) for x in (v, v2))
     assert t.equal(a[:far], b[:far])
+
+
+def test_keys_and_queries_up_to_the_f16_range_of_a_rebuilt_cache():
+    """The last values that F16 holds, in a key and in a query of a quantized cache's 16-bit tail."""
+    t = P.torch()
+    n = 40
+    k, v = P.kv(7, [n], 1)
+    k[3, 0, 5] = 65280.0  # the largest BF16 number below 65520
+    k[4, 0, 5] = -65280.0
+    c = P.cache("q8_0", [n], 1, k, v, tail=64)
+    q = P.queries(7, 4, 2, t.bfloat16)
+    q[..., 5] = 0.0
+    q[1, 1, 6] = 65280.0
+    out, lse = c.batch_attn(0, [0], [4], q, return_lse=True, softmax_scale=1e-4)
+    assert bool(t.isfinite(out).all()) and bool(t.isfinite(lse).all())
+    ref = P.attention(q, *P.cached(c, 0, 0), False, 1e-4)
+    P.check_attention(out, lse, ref, n, P.U16, True)
