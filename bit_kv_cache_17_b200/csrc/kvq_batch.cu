@@ -25,7 +25,7 @@ constexpr float LN2 = 0.6931471805599453f;
 
 // One entry: nq query tokens from row token q0 on, over the first n rows of stream `slot`.
 struct BEntry {
-  int32_t slot, seq, nq;
+  int32_t slot, nq;
   int32_t out;      // position in the call's list (mass rows)
   int64_t n, q0;
   int32_t nblk;     // blocks of query tokens
@@ -54,7 +54,6 @@ struct BArgs {
   int32_t ne, hkv, G, causal, io_f16;
   float qscale;  // softmax scale * log2(e)
   Source src;
-  const uint16_t *q;
   uint16_t *out;
   float *lse;
   const float *mass_in;
@@ -66,11 +65,6 @@ struct BArgs {
   BEntry e[MAXE];
 };
 
-__device__ __forceinline__ void load4(const uint16_t *p, int f16, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(p);
-  const float2 a = ring2f(v.x, f16), b = ring2f(v.y, f16);
-  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-}
 // ---- attention ------------------------------------------------------------------------------------
 //
 // One CTA per (entry, KV head, block of query tokens, split of the key tiles).  A tile of 128 rows
@@ -1056,7 +1050,7 @@ __global__ void __launch_bounds__(256) k_mass_join(const __grid_constant__ BArgs
 // (lane part p: channels 4 p + 32 j + (0..3), j = 0..3: one 32-bit word of the stored planes per
 // block).  Keys are kept as an F16 high part and the F16 remainder (22 bits: a score is an exponent, and
 // the log-sum-exp and the weights are fp32 results); values, whose result is rounded to 16 bits, as one F16.  Bound: the stores
-// (9.2 k tokens of 8 heads, q8_0, K and V in one launch: 18 us for 72 MB written, 20 MB read).
+// (9217 tokens of 8 heads, q8_0, K and V in one launch: 18 us for 57 MB written, 20 MB read).
 // The blocks behind the slots' turn BF16 queries into F16 rows for the products (exact in the F16 range).
 constexpr int MAXR = 128;  // slots per launch
 struct Rebuild {
@@ -1318,7 +1312,6 @@ int make_plan(const kvq_cache *c, int layer, int n_seqs, const int32_t *seq_ids,
     if (n > INT32_MAX - 256) return KVQ_E_UNSUPPORTED;
     if (causal && n_q[i] > n) return KVQ_E_INVAL;
     BEntry e{};
-    e.seq = s;
     e.slot = s;
     e.nq = n_q[i];
     e.out = i;
@@ -1558,7 +1551,6 @@ extern "C" int kvq_batch_attn(kvq_cache *c, int32_t layer, int32_t n_seqs, const
   A.causal = causal;
   A.io_f16 = c->p.tail_f16;
   A.qscale = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)D)) * LOG2E;
-  A.q = static_cast<const uint16_t *>(q);
   A.out = static_cast<uint16_t *>(out);
   A.lse = lse;
   A.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + P.rebuilt_bytes);
@@ -1624,7 +1616,6 @@ extern "C" int kvq_attn_mass(kvq_cache *c, int32_t layer, int32_t n_seqs, const 
   A.causal = causal;
   A.io_f16 = c->p.tail_f16;
   A.qscale = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)D)) * LOG2E;
-  A.q = static_cast<const uint16_t *>(q);
   A.lse = const_cast<float *>(lse);
   A.mass_in = mass_in;
   A.mass_out = mass_out;
