@@ -410,10 +410,10 @@ class KVCache:
         self._ws = None
         self._ws_bytes = {}  # (n_seqs, n_q_heads) -> kvq_workspace_bytes
 
-    def __del__(self):
+    def __del__(self, destroy=_lib.kvq_cache_destroy):  # (this module's names are gone when the interpreter ends)
         h = getattr(self, "handle", None)
         if h:
-            kvq_cache_destroy(h)
+            destroy(h)
             self.handle = None
 
     def _stream(self, stream):
