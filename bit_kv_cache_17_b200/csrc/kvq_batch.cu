@@ -83,15 +83,16 @@ struct BArgs {
 //    only agree, by one barrier with an OR, that none is due.
 // Weights are rounded to the 16-bit type of the product (V's), the sum l is of the unrounded ones.  F16 weights
 // are 2^7 times as large (below 2^15): what falls under the normal range there is off by 2^-32 of the row's
-// largest weight at most, not 2^-25, which many faint tokens would add up (l, O and the records know nothing of it).
+// largest weight at most, not 2^-25, which many faint tokens would add up (l and the results are scaled back).
 // Entries whose rows fill no more than one tile, which latency or HBM bounds, multiply the weights' remainders
 // too and are as exact as their output's type, whatever else is in the call (replays, rounded weights and then
-// these, BF16, 8 KV heads: one row over 4096 tokens 15.2 and 16.5 us, 16 384: 23.1 and 24.8, 65 536: 54.7 and
-// 55.3, 131 072: 94.8 and 94.0; 400 calls in a row, which the power limit slows: 65 536: 54.9 and 55.7, 131 072:
-// 98 and 108).  With two tiles they cost 6 % and more (causal 8k prompt 613 us for 577).
+// these, BF16, 8 KV heads: one row over 4096 tokens 15.3 and 16.4 us, 16 384: 23.3 and 24.5, 65 536: 53.8 and
+// 53.6, 131 072: 93.3 and 93.4; 400 calls in a row, which the power limit slows: 65 536: 53.2 and 53.8, 131 072:
+// 95 and 101).  With two tiles they cost 6 % and more (causal 8k prompt 613 us for 577).
 // Bound, many rows: the chain scores -> maximum -> exponentials -> weights of a tile against the other
-// group's products (causal 8k prompt of 40 heads, F16: 577 us, 1190 TFLOP/s; tensor pipe 53 %, exponentials
-// 48 %).  Bound, one row: HBM (65 536 tokens, 268 MB: 48 us + the join, 5.0 TB/s).
+// group's products (causal 8k prompt of 40 heads, F16: 581 us, 1183 TFLOP/s in replays with pauses, 660 to 690
+// in a stream of calls, which the power limit slows; tensor pipe 53 %, exponentials 48 %).  Bound, one row:
+// HBM (65 536 tokens, 268 MB: 50 us + the join, 4.9 TB/s).
 constexpr int BT = 128;            // rows of a query tile, tokens of a key tile
 constexpr int NSOFT = 16;          // softmax warps
 constexpr int W_MMA = 16, W_LOAD = 17;
@@ -142,13 +143,16 @@ struct Ring {
   }
 };
 
-// LO: the keys have remainders (a rebuilt cache).  ROWS: the query rows of no entry (ONE) or of every entry
-// (MORE) fill more than one tile, or of some (ANY: the choice of the weights by entry costs 6 % of MORE).
-enum Rows { ONE, MORE, ANY };
-template <bool F16, bool LO, Rows ROWS>
-__global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
-                                                const __grid_constant__ CUtensorMap qmap,
-                                                const __grid_constant__ BArgs A) {
+// The entry of this CTA.
+__device__ __forceinline__ const BEntry &entry_of(const BArgs &A) {
+  int ei = 0;
+  while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
+  return A.e[ei];
+}
+
+// LO: the keys have remainders (a rebuilt cache).  ONE: the query rows of the entry fill no more than one tile.
+template <bool F16, bool LO, bool ONE>
+__device__ __forceinline__ void attend(const CUtensorMap &map, const CUtensorMap &qmap, const BArgs &A) {
   extern __shared__ __align__(1024) uint8_t S[];
   const uint32_t base = tc::smem_u32(S);
   if (base & 1023u) {  // the swizzled tiles need it; no launch gives anything else
@@ -162,16 +166,13 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
     tc::prefetch_map(&map);
   }
   if (warp == W_MMA) tc::tmem_alloc(tc::smem_u32(&C.tmem), 512);
-  int ei = 0;
-  while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
-  const BEntry &e = A.e[ei];
+  const BEntry &e = entry_of(A);
   const int G = A.G, hq = A.hkv * G, TB = BT / G;
   const int local = blockIdx.x - e.cta0;
   const int sp = local % e.nsplit, head = local / e.nsplit % A.hkv;
   const int blk = e.nblk - 1 - local / e.nsplit / A.hkv;  // the last (causal: longest) first
   const int tok0 = blk * 2 * TB, tok1 = min(e.nq, tok0 + 2 * TB);
-  const bool halves = ROWS == ONE || tok1 - tok0 <= TB;
-  const bool rem = ROWS == ONE || (ROWS == ANY && e.nq <= TB);  // the weights' remainders are multiplied too
+  const bool halves = ONE || tok1 - tok0 <= TB;
   const int ntile = halves ? 1 : 2;  // query tiles
   const int64_t lim_max = limit_of(A, e, tok1 - 1);
   const int kt = (int)((lim_max + BT - 1) / BT);
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
             for (int s = 0; s < 4; ++s)
               tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 8 * s, v + (uint64_t)((4 * h + s) * (2048 >> 4)), idO,
                          h == 0 && s == 0 ? acc : 1u);
-            if (rem) {
+            if (ONE) {
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 tc::mma_ts(tm + 2 * BT + D * t, tm + BT * t + 64 * h + 32 + 8 * s,
@@ -453,8 +454,8 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       const float sub = m == -INFINITY ? 0.f : (F16 ? LIFT - m : -m);
       const tc::f2 sc = tc::pack2(A.qscale, A.qscale), ms = tc::pack2(sub, sub);
       tc::f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
-      // P over the scores this thread has read; where they count the weights' remainders behind it
-      if (rem) {
+      // P over the scores this thread has read; with ONE the weights' remainders behind it
+      if constexpr (ONE) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t hi[8], lo16[8];
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
       tc::fence_after();
     }
     // halves: group 1 leaves its own in the stages (all consumed), group 0 joins the two
-    const bool one = ROWS == ONE || C.halves, join = one && tiles > 1, split = C.nsplit > 1;
+    const bool one = ONE || C.halves, join = one && tiles > 1, split = C.nsplit > 1;
     float *ex = reinterpret_cast<float *>(S + (one ? 1 : 2) * TILE);  // [128 rows][129], then m and l
     if (join && t == 1) {
 #pragma unroll 1
@@ -606,6 +607,20 @@ __global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensor
   if (warp == W_MMA) tc::tmem_free(tm, 512);
 }
 
+// A launch of entries of one tile of rows (ONE), of more (MORE), or of both (ANY), whose CTAs take either body
+// (31 entries of one row and one of 512 over 4096 tokens: 163 us, with the choice inside one body 168, all
+// weights rounded 151; 7 of one row and one of 2048 over 8192: 371, 408, 367).
+enum Rows { ONE, MORE, ANY };
+template <bool F16, bool LO, Rows ROWS>
+__global__ void __launch_bounds__(NT, 1) k_attn(const __grid_constant__ CUtensorMap map,
+                                                const __grid_constant__ CUtensorMap qmap,
+                                                const __grid_constant__ BArgs A) {
+  if (ROWS == ONE || (ROWS == ANY && entry_of(A).nq <= BT / A.G))
+    attend<F16, LO, true>(map, qmap, A);
+  else
+    attend<F16, LO, false>(map, qmap, A);
+}
+
 // Joins the splits of a row (log-sum-exp, in split order): a block per (query token, query head), a
 // thread per channel, all splits' loads in flight.  Set up behind the attention, waiting only for it.
 __global__ void __launch_bounds__(D) k_attn_join(const __grid_constant__ BArgs A) {
@@ -675,7 +690,7 @@ __global__ void __launch_bounds__(D) k_attn_join(const __grid_constant__ BArgs A
 // Query tiles come by TMA as [token][head] rows of 64 channels, the tokens spread evenly over the
 // tiles; only the columns that hold queries are exponentiated, in steps of 8.
 // 32 queries over 65 536 tokens: 45 us (134 MB; exponentials and products take turns); every query of
-// prompts of 4096 and 512 tokens: 152 us (exponential unit 65 % busy).
+// prompts of 4096 and 512 tokens: 150 us (exponential unit 64 % busy).
 constexpr int NKS = 4, NQS = 3;  // key and query stages
 constexpr int OFF_MCTL = (NKS + NQS) * TILE;
 
@@ -706,9 +721,7 @@ __global__ void __launch_bounds__(NT, 1) k_mass(const __grid_constant__ CUtensor
   }
   MCtl &C = *reinterpret_cast<MCtl *>(S + OFF_MCTL);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(FULL, tid >> 5, 0);
-  int ei = 0;
-  while (ei + 1 < A.ne && A.e[ei + 1].cta0 <= (int)blockIdx.x) ++ei;
-  const BEntry &e = A.e[ei];
+  const BEntry &e = entry_of(A);
   const int G = A.G, hq = A.hkv * G, TB = e.mtb, box = BT / G;  // tokens of a tile, of a copy
   const int local = blockIdx.x - e.cta0;
   const int qs = local % e.mqs, head = local / e.mqs % A.hkv;
